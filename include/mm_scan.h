@@ -1,7 +1,7 @@
 /*
  * mm_scan.h -- C ABI of libmmscan.so: the forward selective scan of Mamba-1
  * with the Momentum Mamba extension, and its Mamba-2 scalar-A chunked (SSD)
- * form, on NVIDIA B200 (sm_100a).
+ * form, the gated delta rule and layer norm, on NVIDIA B200 (sm_100a).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -708,6 +708,158 @@ mm_status mm_scan_fwd_noalloc(const void *x, const void *delta, const float *A,
                               float beta, float alpha,
                               void *y, float *hT, float *vT,
                               const mm_scan_dims *dims, void *stream);
+
+/*
+ * The gated delta rule: the linear recurrence whose state is corrected
+ * towards v along k before it is read.  Like the SSD form it carries a state
+ * (headdim P, dstate N) per batch row and head; q and k take the places of C
+ * and B, v that of x.  (An addition of this library: the pages name the
+ * method beside the selective scan and give no formulas.)
+ *
+ * For every batch row b and head h (group G_h = h / (H / G)), S_{-1} = h0:
+ *     S_t = exp(g_t) S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T
+ *     o_t = scale S_t q_t
+ * that is: S <- exp(g_t) S, u = beta_t (v_t - S k_t), S <- S + u k_t^T.
+ */
+typedef struct {
+    int64_t batch;    /* b                                                  */
+    int64_t seqlen;   /* L (1 for mm_gdr_step)                              */
+    int64_t nheads;   /* H                                                  */
+    int64_t headdim;  /* P: rows of the state, the width of v and o         */
+    int64_t dstate;   /* N: columns of the state, the width of q and k      */
+    int64_t ngroups;  /* G: q/k groups; head h reads group h / (H / G)      */
+    int32_t io;       /* mm_dtype of q, k, v, g, beta, o and their gradients */
+} mm_gdr_dims;
+
+/*
+ * mm_gdr_fwd -- the gated delta rule over a sequence, in chunks of 64 steps.
+ *
+ * Arguments (device buffers unless noted; io is MM_BF16):
+ *   q, k   (batch, L, G, N)  io
+ *   v      (batch, L, H, P)  io
+ *   g      (batch, L, H)     io    log of the decay, <= 0; -inf clears the state
+ *   beta   (batch, L, H)     io    write strength, usually in [0, 1]
+ *   h0     (batch, H, P, N)  fp32  initial state or NULL (zero)
+ *   scale  host scalar, finite     usually 1 / sqrt(N)
+ *   o      (batch, L, H, P)  io    output, rounded to nearest even
+ *   hT     (batch, H, P, N)  fp32  final state or NULL; may equal h0
+ *   ckpt   NULL, or mm_gdr_ckpt_size bytes that mm_gdr_bwd reads: per chunk
+ *          its 64 x 64 products and decays, the state at its start and the
+ *          rows u it wrote (bf16; 1 KB a step and head at P = N = 128)
+ *   workspace  mm_gdr_fwd_workspace_size bytes, overwritten, not used by
+ *          anything else until the call's work on `stream` has completed
+ * The recurrence is stable for |k| <= 1 with beta in [0, 2]; k is not
+ * normalised here.  The state is fp32: where it enters a matrix product it is
+ * split in two bf16 terms, so hT is accurate to a few 1e-6 of its size; o
+ * carries bf16 rounding of the products that reach it alone.  Padding a
+ * batch row on the right changes nothing before the padding; its steps are
+ * steps like any other for hT (give them beta = 0 and g = 0 to keep the state).
+ * Streaming: calls split at a multiple of 64, with hT of the first as h0 of
+ * the second, reproduce o and hT bit for bit.
+ * Nothing is allocated; the calls can be captured into a CUDA graph (the
+ * workspace then belongs to the graph).
+ *
+ * Supported sizes: headdim and dstate each 64 or 128, seqlen up to 2^30,
+ * batch * nheads * ceil(seqlen / 64) < 2^31.
+ * Errors: MM_ERR_NULL (q, k, v, g, beta, o, workspace or dims), MM_ERR_DIMS
+ * (a size < 1, H not a multiple of G, workspace too small), MM_ERR_DTYPE (io
+ * not MM_BF16), MM_ERR_SCALAR (scale), MM_ERR_UNSUPPORTED, MM_ERR_ALIGN,
+ * MM_ERR_ALIAS (an output, ckpt and workspace among them, over an input or
+ * another output, except hT == h0), MM_ERR_CUDA.
+ */
+mm_status mm_gdr_fwd(const void *q, const void *k, const void *v,
+                     const void *g, const void *beta, const float *h0,
+                     float scale, void *o, float *hT, void *ckpt,
+                     void *workspace, size_t workspace_bytes,
+                     const mm_gdr_dims *dims, void *stream);
+
+/* Bytes of mm_gdr_fwd's workspace (with_ckpt != 0: when ckpt is given), of
+ * its checkpoint buffer, and of mm_gdr_bwd's workspace.  Errors as the size
+ * checks of mm_gdr_fwd; MM_ERR_NULL. */
+mm_status mm_gdr_fwd_workspace_size(const mm_gdr_dims *dims, int with_ckpt, size_t *bytes);
+mm_status mm_gdr_ckpt_size(const mm_gdr_dims *dims, size_t *bytes);
+mm_status mm_gdr_bwd_workspace_size(const mm_gdr_dims *dims, size_t *bytes);
+
+/*
+ * mm_gdr_bwd -- gradients of mm_gdr_fwd.
+ *
+ * Inputs: q, k, v, g, beta, scale, dims as given to the forward; ckpt as it
+ * wrote it for them (it holds h0's part); dout (batch, L, H, P) io, the
+ * gradient reaching o; dhT (batch, H, P, N) fp32, the gradient reaching hT,
+ * or NULL for zero.
+ * Outputs (overwritten): dq, dk (batch, L, G, N), summed over the heads of a
+ * group; dv (batch, L, H, P); dg, dbeta (batch, L, H), all io; dh0 (batch, H,
+ * P, N) fp32 or NULL.  Every output is bit-identical from run to run.
+ * Products take their operands rounded to bf16, with fp32 sums; dh0, though
+ * fp32, has that accuracy (a few 1e-3 of its size).
+ * Errors: as mm_gdr_fwd.
+ */
+mm_status mm_gdr_bwd(const void *q, const void *k, const void *v,
+                     const void *g, const void *beta, float scale,
+                     const void *ckpt, const void *dout, const float *dhT,
+                     void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                     float *dh0, void *workspace, size_t workspace_bytes,
+                     const mm_gdr_dims *dims, void *stream);
+
+/*
+ * mm_gdr_step -- one decode step of the gated delta rule on cached states,
+ * updated in place (the L = 1 case, in fp32 arithmetic).
+ *   q, k (batch, G, N), v, o (batch, H, P), g, beta (batch, H) io (fp32 or
+ *   bf16); h (batch, H, P, N) fp32, read and overwritten; dims->seqlen 1.
+ * Supported sizes: any headdim, dstate a multiple of 4 up to 256.
+ * Errors: as mm_gdr_fwd; MM_ERR_DIMS for seqlen != 1.
+ */
+mm_status mm_gdr_step(const void *q, const void *k, const void *v,
+                      const void *g, const void *beta, float *h, float scale,
+                      void *o, const mm_gdr_dims *dims, void *stream);
+
+/* Sizes of one layer norm call. */
+typedef struct {
+    int64_t rows;    /* independent rows                                     */
+    int64_t cols;    /* elements a row is normalised over, 1 .. 16384        */
+    int32_t io;      /* mm_dtype of x, z, y, dy, dx and dz                   */
+} mm_norm_dims;
+
+/*
+ * mm_layer_norm_fwd -- layer norm of the rows of x, with an optional gate
+ * as in the scan's output (silu(z), see mm_scan_fwd_gated):
+ *     y = ((x - mean) rstd weight + bias) * z * sigmoid(z)
+ *     rstd = 1 / sqrt(var + eps), mean and var over the row's cols elements
+ * rms != 0: mean is 0 and var the mean of the squares (RMS norm).
+ *   x, z, y (rows, cols) io; weight, bias (cols) fp32; mean, rstd (rows)
+ *   fp32 outputs, which mm_layer_norm_bwd reads.  weight (ones), bias
+ *   (zeros), z (no gate), mean and rstd may be NULL; mean is not written
+ *   with rms.
+ *   eps    host scalar, finite, >= 0
+ * Arithmetic is fp32; the variance is summed over centred elements.
+ * Errors: MM_ERR_NULL (x, y, dims), MM_ERR_DIMS (a size < 1), MM_ERR_DTYPE,
+ * MM_ERR_SCALAR (eps), MM_ERR_UNSUPPORTED (cols > 16384, rows >= 2^31),
+ * MM_ERR_ALIGN, MM_ERR_ALIAS, MM_ERR_CUDA.
+ */
+mm_status mm_layer_norm_fwd(const void *x, const float *weight, const float *bias,
+                            const void *z, float eps, int rms,
+                            void *y, float *mean, float *rstd,
+                            const mm_norm_dims *dims, void *stream);
+
+/* Bytes of mm_layer_norm_bwd's workspace (partial sums of dweight, dbias). */
+mm_status mm_layer_norm_bwd_workspace_size(const mm_norm_dims *dims, size_t *bytes);
+
+/*
+ * mm_layer_norm_bwd -- gradients of mm_layer_norm_fwd.  x, weight, bias, z,
+ * rms as given to it, mean and rstd as it wrote them (mean NULL with rms); dy
+ * (rows, cols) io.  Outputs (overwritten): dx (rows, cols) io; dz like z;
+ * dweight, dbias (cols) fp32, sums over the rows in a fixed order, bit-identical
+ * from run to run; dz, dweight and dbias may be NULL (not formed).
+ * workspace: mm_layer_norm_bwd_workspace_size bytes (NULL allowed when
+ * dweight and dbias are NULL).
+ * Errors: as mm_layer_norm_fwd; MM_ERR_NULL also for dz without z,
+ * MM_ERR_DIMS for a workspace that is too small.
+ */
+mm_status mm_layer_norm_bwd(const void *x, const float *weight, const float *bias,
+                            const void *z, int rms, const float *mean, const float *rstd,
+                            const void *dy, void *dx, float *dweight, float *dbias, void *dz,
+                            void *workspace, size_t workspace_bytes,
+                            const mm_norm_dims *dims, void *stream);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int mm_version(void);

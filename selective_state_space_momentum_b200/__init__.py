@@ -13,6 +13,11 @@ Convenience wrappers allocate outputs:
   Mamba page's ``selective_scan_fn`` with D, z, delta_bias unset and no
   softplus on delta.
 * :func:`ssd_fwd` -- ``(y, last_state)`` of the multi-head scalar-A form.
+* :func:`gdr_fwd`, :func:`gdr_fwd_train`, :func:`gdr_bwd`, :func:`gdr_step` --
+  the gated delta rule in the SSD layout: over a sequence, its gradients and
+  one decode step.
+* :func:`layer_norm_fwd`, :func:`layer_norm_bwd` -- layer (or RMS) norm over
+  the last dimension with an optional gate, and its gradients.
 * :func:`scan_fwd_host` -- end-to-end call on host arrays (copies in, scan,
   copies out) for callers whose data lives in host memory.
 * :func:`scan_fwd_split` -- one sequence cut into pieces over the ranks of a
@@ -38,6 +43,9 @@ __all__ = [
     "mm_ipc_close_handle", "SplitPeers", "mm_device_status", "scan_fwd", "scan_fwd_train", "scan_bwd", "ssd_fwd", "scan_fwd_host",
     "ssd_fwd_host", "split_pieces", "scan_fwd_split", "scan_fwd_split_peers",
     "EXPORTED_SYMBOLS", "MM_SCAN_CKPT_STEPS",
+    "mm_gdr_fwd", "mm_gdr_fwd_workspace_size", "mm_gdr_ckpt_size", "mm_gdr_bwd", "mm_gdr_bwd_workspace_size",
+    "mm_gdr_step", "gdr_fwd", "gdr_fwd_train", "gdr_bwd", "gdr_step",
+    "mm_layer_norm_fwd", "mm_layer_norm_bwd", "mm_layer_norm_bwd_workspace_size", "layer_norm_fwd", "layer_norm_bwd",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -66,7 +74,10 @@ EXPORTED_SYMBOLS = ("mm_scan_fwd", "mm_scan_fwd_gated", "mm_scan_ckpt_size", "mm
                     "mm_ssd_fwd_host_workspace_size", "mm_ssd_fwd_host",
                     "mm_scan_split_maps_size", "mm_scan_fwd_split_maps", "mm_scan_fwd_split_correct",
                     "mm_scan_fwd_noalloc", "mm_scan_fwd_split_maps_peers", "mm_ipc_get_handle",
-                    "mm_ipc_open_handle", "mm_ipc_close_handle")
+                    "mm_ipc_open_handle", "mm_ipc_close_handle",
+                    "mm_gdr_fwd", "mm_gdr_fwd_workspace_size", "mm_gdr_ckpt_size", "mm_gdr_bwd",
+                    "mm_gdr_bwd_workspace_size", "mm_gdr_step", "mm_layer_norm_fwd", "mm_layer_norm_bwd",
+                    "mm_layer_norm_bwd_workspace_size")
 
 
 class MMError(RuntimeError):
@@ -87,6 +98,16 @@ class SSDDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("ngroups", ctypes.c_int64), ("chunk", ctypes.c_int64)]
+
+
+class GDRDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("io", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("io", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -149,6 +170,19 @@ def _declare(lib):
     lib.mm_ipc_close_handle.argtypes = [vp, i64]
     lib.mm_scan_fwd_noalloc.restype = ctypes.c_int
     lib.mm_scan_fwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, f, f, vp, vp, vp, ctypes.POINTER(ScanDims), vp]
+    gdr, norm, size_out = ctypes.POINTER(GDRDims), ctypes.POINTER(NormDims), ctypes.POINTER(sz)
+    for name, argtypes in (
+            ("mm_gdr_fwd", [vp] * 6 + [f] + [vp] * 4 + [sz, gdr, vp]),
+            ("mm_gdr_fwd_workspace_size", [gdr, ctypes.c_int, size_out]),
+            ("mm_gdr_ckpt_size", [gdr, size_out]),
+            ("mm_gdr_bwd", [vp] * 5 + [f] + [vp] * 10 + [sz, gdr, vp]),
+            ("mm_gdr_bwd_workspace_size", [gdr, size_out]),
+            ("mm_gdr_step", [vp] * 6 + [f, vp, gdr, vp]),
+            ("mm_layer_norm_fwd", [vp] * 4 + [f, ctypes.c_int] + [vp] * 3 + [norm, vp]),
+            ("mm_layer_norm_bwd", [vp] * 4 + [ctypes.c_int] + [vp] * 8 + [sz, norm, vp]),
+            ("mm_layer_norm_bwd_workspace_size", [norm, size_out])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = argtypes
     lib.mm_status_string.restype = ctypes.c_char_p
     lib.mm_status_string.argtypes = [ctypes.c_int]
     lib.mm_last_error.restype = ctypes.c_char_p
@@ -1025,3 +1059,266 @@ def scan_fwd_split_peers(x, delta, A, B, C, seg_len, seqlen_total, peers, h0=Non
     mm_scan_fwd_split_correct(delta, A, C, h0, v0, beta, alpha, y, hT, vT, local, seg_len, first,
                               seqlen_total, stream)
     return y, hT, vT
+
+
+# ------------------------------------------- gated delta rule, layer norm -----
+# The kernels run on the device that is current when they are launched; these
+# wrappers make the operands' device current for the call, and take that
+# device's current stream by default.
+def _launch(device, stream, call):
+    import torch
+    with torch.cuda.device(device):
+        return call(_stream_handle(stream))
+
+
+def _bytes_of(fn, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(getattr(load_library(), fn)(*args, ctypes.byref(out)), fn)
+    return int(out.value)
+
+
+def _require_bytes(name, t, nbytes, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous uint8 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the operands on {device}")
+    if t.numel() < nbytes:
+        raise ValueError(f"{name} holds {t.numel()} bytes; the call needs {nbytes}")
+
+
+def _gdr_dims(q, k, v, g, beta, tensors, step=False):
+    """v (batch[, L], H, P) and q (batch[, L], G, N) fix the sizes; `tensors`
+    is a list of (name, tensor, kind, optional), kind v, qk, gate or state."""
+    import torch
+    load_library()
+    dev, io = _lead(v, 3 if step else 4, "v")
+    if not step and io != torch.bfloat16:
+        raise TypeError("the gated delta rule over a sequence takes bf16 q, k, v, g, beta and o")
+    if not isinstance(q, torch.Tensor) or q.dim() != v.dim():
+        raise ValueError(f"q must be a {v.dim()}-D tensor like v")
+    lead, (H, P), (G, N) = tuple(v.shape[:-2]), v.shape[-2:], q.shape[-2:]
+    shapes = {"qk": (lead + (G, N), (io,)), "v": (lead + (H, P), (io,)), "gate": (lead + (H,), (io,)),
+              "state": ((v.shape[0], H, P, N), (torch.float32,))}
+    for name, t, kind, optional in [("q", q, "qk", False), ("k", k, "qk", False), ("g", g, "gate", False),
+                                    ("beta", beta, "gate", False)] + tensors:
+        shape, dts = shapes[kind]
+        _require(name, t, shape, dts, dev, optional)
+    _on_cuda(dev)
+    return GDRDims(v.shape[0], 1 if step else v.shape[1], H, P, N, G, _io_code(io))
+
+
+def mm_gdr_fwd_workspace_size(batch, seqlen, nheads, headdim, dstate, ngroups, with_ckpt=False) -> int:
+    """C entry point mm_gdr_fwd_workspace_size: bytes of mm_gdr_fwd's workspace."""
+    dims = GDRDims(batch, seqlen, nheads, headdim, dstate, ngroups, MM_BF16)
+    return _bytes_of("mm_gdr_fwd_workspace_size", ctypes.byref(dims), 1 if with_ckpt else 0)
+
+
+def mm_gdr_ckpt_size(batch, seqlen, nheads, headdim, dstate, ngroups) -> int:
+    """C entry point mm_gdr_ckpt_size: bytes of the buffer mm_gdr_bwd restarts from."""
+    return _bytes_of("mm_gdr_ckpt_size", ctypes.byref(GDRDims(batch, seqlen, nheads, headdim, dstate, ngroups, MM_BF16)))
+
+
+def mm_gdr_bwd_workspace_size(batch, seqlen, nheads, headdim, dstate, ngroups) -> int:
+    """C entry point mm_gdr_bwd_workspace_size: bytes of mm_gdr_bwd's workspace."""
+    return _bytes_of("mm_gdr_bwd_workspace_size",
+                     ctypes.byref(GDRDims(batch, seqlen, nheads, headdim, dstate, ngroups, MM_BF16)))
+
+
+def mm_gdr_fwd(q, k, v, g, beta, h0, scale, o, hT, ckpt, workspace, stream=None):
+    """C entry point mm_gdr_fwd on torch CUDA tensors (marshalling only).
+
+    q, k (batch, L, G, N), v, o (batch, L, H, P), g, beta (batch, L, H) bf16;
+    h0, hT (batch, H, P, N) fp32 or None; ckpt (mm_gdr_ckpt_size bytes, or
+    None) and workspace (mm_gdr_fwd_workspace_size bytes) uint8.
+    """
+    dims = _gdr_dims(q, k, v, g, beta, [("h0", h0, "state", True), ("o", o, "v", False), ("hT", hT, "state", True)])
+    ref, lib = ctypes.byref(dims), load_library()
+    if ckpt is not None:
+        _require_bytes("ckpt", ckpt, _bytes_of("mm_gdr_ckpt_size", ref), v.device)
+    _require_bytes("workspace", workspace, _bytes_of("mm_gdr_fwd_workspace_size", ref, 0 if ckpt is None else 1), v.device)
+    _check(_launch(v.device, stream, lambda s: lib.mm_gdr_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), float(scale), _ptr(o), _ptr(hT), _ptr(ckpt),
+        _ptr(workspace), workspace.numel(), ref, s)), "mm_gdr_fwd")
+
+
+def mm_gdr_bwd(q, k, v, g, beta, scale, ckpt, dout, dhT, dq, dk, dv, dg, dbeta, dh0, workspace, stream=None):
+    """C entry point mm_gdr_bwd on torch CUDA tensors (marshalling only): the
+    gradients have the shapes and types of q, k, v, g, beta and h0."""
+    dims = _gdr_dims(q, k, v, g, beta, [("dout", dout, "v", False), ("dhT", dhT, "state", True), ("dq", dq, "qk", False),
+                                        ("dk", dk, "qk", False), ("dv", dv, "v", False), ("dg", dg, "gate", False),
+                                        ("dbeta", dbeta, "gate", False), ("dh0", dh0, "state", True)])
+    ref, lib = ctypes.byref(dims), load_library()
+    _require_bytes("ckpt", ckpt, _bytes_of("mm_gdr_ckpt_size", ref), v.device)
+    _require_bytes("workspace", workspace, _bytes_of("mm_gdr_bwd_workspace_size", ref), v.device)
+    _check(_launch(v.device, stream, lambda s: lib.mm_gdr_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(ckpt), _ptr(dout), _ptr(dhT), _ptr(dq), _ptr(dk),
+        _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), _ptr(workspace), workspace.numel(), ref, s)), "mm_gdr_bwd")
+
+
+def mm_gdr_step(q, k, v, g, beta, h, scale, o, stream=None):
+    """C entry point mm_gdr_step (marshalling only): one decode step.
+
+    q, k (batch, G, N), v, o (batch, H, P), g, beta (batch, H) in one storage
+    type (fp32 or bf16); h (batch, H, P, N) fp32, updated in place.
+    """
+    dims = _gdr_dims(q, k, v, g, beta, [("h", h, "state", False), ("o", o, "v", False)], step=True)
+    lib = load_library()
+    _check(_launch(v.device, stream, lambda s: lib.mm_gdr_step(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h), float(scale), _ptr(o), ctypes.byref(dims), s)), "mm_gdr_step")
+
+
+def _gdr_outputs(v, q, return_last_state, with_ckpt):
+    import torch
+    if not isinstance(v, torch.Tensor) or v.dim() != 4 or not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q and v must be 4-D (batch, L, heads, width) tensors")
+    sizes = (v.shape[0], v.shape[1], v.shape[2], v.shape[3], q.shape[3], q.shape[2])
+    dev = v.device
+    hT = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), device=dev, dtype=torch.float32) if return_last_state else None
+    ckpt = torch.empty(mm_gdr_ckpt_size(*sizes), device=dev, dtype=torch.uint8) if with_ckpt else None
+    return torch.empty_like(v), hT, ckpt, torch.empty(mm_gdr_fwd_workspace_size(*sizes, with_ckpt), device=dev, dtype=torch.uint8)
+
+
+def gdr_fwd(q, k, v, g, beta, h0=None, scale=None, return_last_state=True, stream=None):
+    """The gated delta rule over a sequence: allocate outputs and workspace and
+    run mm_gdr_fwd; returns (o, hT) (hT None when ``return_last_state`` is
+    False).  scale: 1 / sqrt(N) by default."""
+    o, hT, _, ws = _gdr_outputs(v, q, return_last_state, False)
+    mm_gdr_fwd(q, k, v, g, beta, h0, q.shape[3] ** -0.5 if scale is None else scale, o, hT, None, ws, stream)
+    _hold(stream, o, hT, ws)
+    return o, hT
+
+
+def gdr_fwd_train(q, k, v, g, beta, h0=None, scale=None, return_last_state=False, stream=None):
+    """gdr_fwd that also keeps what the backward needs: returns (o, hT, ckpt),
+    ckpt uint8 (hT None unless ``return_last_state``)."""
+    o, hT, ckpt, ws = _gdr_outputs(v, q, return_last_state, True)
+    mm_gdr_fwd(q, k, v, g, beta, h0, q.shape[3] ** -0.5 if scale is None else scale, o, hT, ckpt, ws, stream)
+    _hold(stream, o, hT, ckpt, ws)
+    return o, hT, ckpt
+
+
+def gdr_bwd(q, k, v, g, beta, ckpt, dout, dhT=None, scale=None, return_dh0=False, stream=None):
+    """Allocate the gradients and run mm_gdr_bwd; returns a dict with dq, dk,
+    dv, dg, dbeta and, with ``return_dh0``, dh0."""
+    import torch
+    if not isinstance(v, torch.Tensor) or v.dim() != 4 or not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q and v must be 4-D (batch, L, heads, width) tensors")
+    sizes = (v.shape[0], v.shape[1], v.shape[2], v.shape[3], q.shape[3], q.shape[2])
+    grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
+             "dbeta": torch.empty_like(beta)}
+    dh0 = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), device=v.device, dtype=torch.float32) if return_dh0 else None
+    ws = torch.empty(mm_gdr_bwd_workspace_size(*sizes), device=v.device, dtype=torch.uint8)
+    mm_gdr_bwd(q, k, v, g, beta, q.shape[3] ** -0.5 if scale is None else scale, ckpt, dout, dhT, *grads.values(), dh0, ws, stream)
+    if return_dh0:
+        grads["dh0"] = dh0
+    _hold(stream, ws, *grads.values())
+    return grads
+
+
+def gdr_step(q, k, v, g, beta, h, scale=None, stream=None):
+    """One decode step of the gated delta rule: h (batch, H, P, N) fp32 is
+    updated in place; returns o (batch, H, P)."""
+    import torch
+    if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q and v must be 3-D (batch, heads, width) tensors")
+    o = torch.empty_like(v)
+    mm_gdr_step(q, k, v, g, beta, h, q.shape[2] ** -0.5 if scale is None else scale, o, stream)
+    _hold(stream, o)
+    return o
+
+
+def _hold(stream, *tensors):
+    """Tensors a wrapper allocated on the current stream and used on another
+    one: the allocator may hand their memory out again only after that
+    stream's work."""
+    import torch
+    if stream is None:
+        return
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _norm_dims(x, weight, bias, z, tensors):
+    """x (..., cols) fixes the sizes; rows are its leading dimensions together."""
+    import torch
+    load_library()
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor with at least one dimension")
+    dev, io = _lead(x, x.dim())
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    f32 = (torch.float32,)
+    shapes = {"io": (tuple(x.shape), (io,)), "col": ((cols,), f32), "row": (tuple(x.shape[:-1]), f32)}
+    for name, t, kind, optional in [("weight", weight, "col", True), ("bias", bias, "col", True), ("z", z, "io", True)] + tensors:
+        shape, dts = shapes[kind]
+        _require(name, t, shape, dts, dev, optional)
+    _on_cuda(dev)
+    return NormDims(rows, cols, _io_code(io))
+
+
+def mm_layer_norm_fwd(x, weight, bias, z, eps, rms, y, mean, rstd, stream=None):
+    """C entry point mm_layer_norm_fwd on torch CUDA tensors (marshalling
+    only): x, z, y (..., cols) in one storage type, weight, bias (cols,) fp32,
+    mean, rstd (...) fp32; weight, bias, z, mean, rstd may be None."""
+    dims = _norm_dims(x, weight, bias, z, [("y", y, "io", False), ("mean", mean, "row", True), ("rstd", rstd, "row", True)])
+    lib = load_library()
+    _check(_launch(x.device, stream, lambda s: lib.mm_layer_norm_fwd(
+        _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), float(eps), 1 if rms else 0, _ptr(y), _ptr(mean), _ptr(rstd),
+        ctypes.byref(dims), s)), "mm_layer_norm_fwd")
+
+
+def mm_layer_norm_bwd_workspace_size(rows, cols, io=MM_F32) -> int:
+    """C entry point mm_layer_norm_bwd_workspace_size."""
+    return _bytes_of("mm_layer_norm_bwd_workspace_size", ctypes.byref(NormDims(rows, cols, io)))
+
+
+def mm_layer_norm_bwd(x, weight, bias, z, rms, mean, rstd, dy, dx, dweight, dbias, dz, workspace, stream=None):
+    """C entry point mm_layer_norm_bwd (marshalling only): dx, dz like x,
+    dweight, dbias (cols,) fp32 or None, workspace uint8 (None when neither
+    dweight nor dbias is asked for)."""
+    dims = _norm_dims(x, weight, bias, z, [("mean", mean, "row", bool(rms)), ("rstd", rstd, "row", False), ("dy", dy, "io", False),
+                                           ("dx", dx, "io", False), ("dweight", dweight, "col", True),
+                                           ("dbias", dbias, "col", True), ("dz", dz, "io", True)])
+    ref, lib = ctypes.byref(dims), load_library()
+    if dweight is not None or dbias is not None:
+        _require_bytes("workspace", workspace, _bytes_of("mm_layer_norm_bwd_workspace_size", ref), x.device)
+    _check(_launch(x.device, stream, lambda s: lib.mm_layer_norm_bwd(
+        _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), 1 if rms else 0, _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dweight),
+        _ptr(dbias), _ptr(dz), _ptr(workspace), 0 if workspace is None else workspace.numel(), ref, s)), "mm_layer_norm_bwd")
+
+
+def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, stream=None):
+    """Layer norm over the last dimension of x (RMS norm with ``rms``), gated
+    by silu(z) when z is given: returns (y, mean, rstd), mean None with rms."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"x must be a torch.Tensor, got {type(x).__name__}")
+    y = torch.empty_like(x)
+    rstd = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+    mean = None if rms else torch.empty_like(rstd)
+    mm_layer_norm_fwd(x, weight, bias, z, eps, rms, y, mean, rstd, stream)
+    _hold(stream, y, mean, rstd)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x, weight, bias, mean, rstd, dy, z=None, rms=False, stream=None):
+    """Allocate the gradients and run mm_layer_norm_bwd: returns a dict with
+    dx and, for each that was given, dweight, dbias, dz."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor with at least one dimension")
+    grads = {"dx": torch.empty_like(x)}
+    for name, t in (("dweight", weight), ("dbias", bias), ("dz", z)):
+        if t is not None:
+            grads[name] = torch.empty_like(t)
+    ws = None
+    if weight is not None or bias is not None:
+        cols = max(1, x.shape[-1])
+        ws = torch.empty(mm_layer_norm_bwd_workspace_size(x.numel() // cols, cols, _io_code(x.dtype)), device=x.device, dtype=torch.uint8)
+    mm_layer_norm_bwd(x, weight, bias, z, rms, mean, rstd, dy, grads["dx"], grads.get("dweight"), grads.get("dbias"), grads.get("dz"),
+                      ws, stream)
+    _hold(stream, ws, *grads.values())
+    return grads

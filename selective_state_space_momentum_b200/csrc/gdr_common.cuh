@@ -1,0 +1,137 @@
+// gdr_common.cuh -- what the chunked gated-delta-rule kernels share: the
+// chunk records, swizzled shared-memory tiles and the warp matrix products.
+#pragma once
+
+#include "mm_common.cuh"
+#include "mm_internal.h"
+
+namespace mmscan {
+namespace gdr {
+
+constexpr int C = kGdrChunk;               // steps of a chunk
+
+// Per (batch row, head, chunk) record, written by the preparing kernel:
+//   T   (C, C) bf16   (I + A)^-1, A_ij = beta_i e^(c_i - c_j) k_i.k_j (j < i),
+//                     c the cumulative g of the chunk
+//   Pm  (C, C) bf16   scale e^(c_i - c_j) q_i.k_j (j <= i)
+//   eg, tail, beta (C) fp32: e^(c_i), e^(c_last - c_i), beta_i
+// and, apart from it, Tlo (C, C) bf16, what T's rounding to bf16 left over.
+constexpr int REC_T = 0, REC_P = C * C * 2, REC_F = 2 * C * C * 2;
+constexpr int REC_BYTES = REC_F + 3 * C * 4;
+static_assert(REC_BYTES == kGdrRecBytes, "record size");
+
+// Tiles in shared memory: rows of 128 or 256 bytes, the 16-byte pieces of a
+// row permuted by the row's number mod 8, so that the eight rows an ldmatrix
+// reads at one column lie in different banks.
+template <int RB>
+__device__ __forceinline__ uint32_t tile_off(int row, int c16) {
+    return (uint32_t)(row * RB + ((c16 ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 :: "r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Operand fragments from a tile; `lane` 0..31, every index in elements of 8
+// (c16) or rows.
+// B (k x n) of two neighbouring n-tiles from a tile stored [n][k] / [k][n].
+template <int RB>
+__device__ __forceinline__ void load_b_nk(uint32_t tile, int n0, int kc, int lane, uint32_t (&r)[4]) {
+    const int m = lane >> 3;
+    ldsm4(tile + tile_off<RB>(n0 + (m >> 1) * 8 + (lane & 7), kc + (m & 1)), r);
+}
+template <int RB>
+__device__ __forceinline__ void load_b_kn(uint32_t tile, int k0, int nc, int lane, uint32_t (&r)[4]) {
+    const int m = lane >> 3;
+    ldsm4t(tile + tile_off<RB>(k0 + (m & 1) * 8 + (lane & 7), nc + (m >> 1)), r);
+}
+// A (16 x 16) from a tile stored [m][k] / [k][m].
+template <int RB>
+__device__ __forceinline__ void load_a_mk(uint32_t tile, int m0, int kc, int lane, uint32_t (&r)[4]) {
+    const int m = lane >> 3;
+    ldsm4(tile + tile_off<RB>(m0 + (m & 1) * 8 + (lane & 7), kc + (m >> 1)), r);
+}
+template <int RB>
+__device__ __forceinline__ void load_a_km(uint32_t tile, int k0, int mc, int lane, uint32_t (&r)[4]) {
+    const int m = lane >> 3;
+    ldsm4t(tile + tile_off<RB>(k0 + (m >> 1) * 8 + (lane & 7), mc + (m & 1)), r);
+}
+
+// The A operand of k-step kt from accumulators c (the product before it).
+template <int NT>
+__device__ __forceinline__ void acc_to_a(const float (&c)[NT][4], int kt, uint32_t (&a)[4]) {
+    a[0] = pack_bf16x2(c[2 * kt][0], c[2 * kt][1]);
+    a[1] = pack_bf16x2(c[2 * kt][2], c[2 * kt][3]);
+    a[2] = pack_bf16x2(c[2 * kt + 1][0], c[2 * kt + 1][1]);
+    a[3] = pack_bf16x2(c[2 * kt + 1][2], c[2 * kt + 1][3]);
+}
+// The same split in two bf16 terms: hi + lo is the fp32 value to 2^-17.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(x, y);
+    lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+template <int NT>
+__device__ __forceinline__ void acc_to_a2(const float (&c)[NT][4], int kt, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(c[2 * kt][0], c[2 * kt][1], hi[0], lo[0]);
+    split2(c[2 * kt][2], c[2 * kt][3], hi[1], lo[1]);
+    split2(c[2 * kt + 1][0], c[2 * kt + 1][1], hi[2], lo[2]);
+    split2(c[2 * kt + 1][2], c[2 * kt + 1][3], hi[3], lo[3]);
+}
+
+// Cumulative g of a chunk in 64 bits, by one warp; lane l gets the sums at
+// rows 2 l and 2 l + 1 and the chunk's last.  The decays are exponentials of
+// differences of these sums, and one strongly negative g would take the low
+// bits of the others' differences in fp32.  Below -1e4 (-inf included) a step
+// forgets everything (e^g = 0 either way): clamped, so that no difference is
+// inf - inf.  `g` points at the chunk's first step, `stride` elements apart.
+__device__ __forceinline__ void chunk_cumsum(const bf16* g, int64_t stride, int valid, int lane, double& s0, double& s1, double& last) {
+    const int r = 2 * lane;
+    s0 = s1 = 0.0;
+    if (r < valid) {
+        const float x = __bfloat162float(g[r * stride]);
+        s0 = x < -1e4f ? -1e4f : x;
+    }
+    if (r + 1 < valid) {
+        const float x = __bfloat162float(g[(r + 1) * stride]);
+        s1 = x < -1e4f ? -1e4f : x;
+    }
+    s1 += s0;
+    double run = s1;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, run, m);
+        if (lane >= m) run += up;
+    }
+    s0 += run - s1;
+    s1 = run;
+    last = __shfl_sync(0xffffffffu, run, 31);
+}
+
+// ROWS rows of RB bytes from global memory (row stride `stride` bytes) into a
+// tile, by all `nthreads` threads; rows from `valid` on become zeros.
+template <int RB, int ROWS>
+__device__ __forceinline__ void load_tile(unsigned char* tile, const void* src, int64_t stride, int valid, int tid, int nthreads) {
+    constexpr int PIECES = RB / 16;
+    for (int i = tid; i < ROWS * PIECES; i += nthreads) {
+        const int r = i / PIECES, c = i % PIECES;
+        const bool in = r < valid;
+        cp_async_16(tile + tile_off<RB>(r, c), static_cast<const unsigned char*>(src) + (in ? r : 0) * stride + c * 16, in ? 16 : 0);
+    }
+}
+
+}  // namespace gdr
+}  // namespace mmscan

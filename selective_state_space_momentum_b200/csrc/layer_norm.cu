@@ -1,0 +1,392 @@
+// layer_norm.cu -- sm_100a kernels for layer norm over the last dimension,
+// forward and backward, with an optional gate.
+//
+// What it computes, per row of x (rows, cols):
+//     xh = (x - mean) rstd,  rstd = 1 / sqrt(var + eps)     (rms: mean = 0)
+//     n  = xh w + b,         y = n silu(z)                  (w, b, z optional)
+// and, with dn = dy silu(z), d = dn w, averages over the row's columns:
+//     dx = rstd (d - avg(d) - xh avg(d xh))                 (rms: no avg(d))
+//     dz = dy n sig(z) (1 + z (1 - sig(z))),  dw = sum_rows dn xh,  db = sum_rows dn
+//
+// Bound: HBM (x, z, dy read once, y, dx, dz written once; a dozen operations
+// an element).  A row is kept in the registers of TPR threads, so that the
+// mean, the centred sum of squares (two passes over registers: no
+// cancellation when the mean is large) and the output take one read of
+// memory.  All statistics and sums are fp32.  TPR is the smallest of 8, 32,
+// 128, 512, 1024 whose threads hold the row in 16 elements each: short rows
+// (a head's 64 channels) share a warp, so each thread still moves 16 bytes
+// at a time and the reductions stay in shuffles.
+//
+// The weight's gradient: a block walks rows in a grid-stride loop with the
+// sums of its columns in registers, writes one partial row to the workspace,
+// and a second kernel adds the partials in block order: no atomics, so the
+// result is bit-identical from run to run.
+#include "mm_common.cuh"
+#include "mm_internal.h"
+
+namespace mmscan {
+
+namespace {
+
+constexpr int kElems = 16;        // elements of a row a thread holds, at most
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.0f, 1.0f + ex2_approx(-z * kLog2e)); }
+
+// VEC consecutive elements, widened to fp32 (16-byte accesses for VEC > 1).
+template <typename IO, int VEC>
+__device__ __forceinline__ void load_vec(const IO* p, float* v) {
+    if constexpr (VEC == 1) {
+        v[0] = load1(p);
+    } else if constexpr (sizeof(IO) == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+        v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+    }
+}
+
+template <typename IO, int VEC>
+__device__ __forceinline__ void store_vec(IO* p, const float* v) {
+    if constexpr (VEC == 1) {
+        store1(p, v[0]);
+    } else if constexpr (sizeof(IO) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_param(const float* p, float* v, float none) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = none;
+    if (!p) return;
+    if constexpr (VEC == 1) {
+        v[0] = *p;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + e);
+            v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+        }
+    }
+}
+
+// Sum of (a, b) over the TPR threads of a row, in every one of them.  Rows of
+// more than a warp go through `red`, one of two slots that alternate from
+// call to call, so that one barrier a call is enough: a slot is written again
+// only after the barrier of the call in between.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 v, float2* red, int& slot) {
+#pragma unroll
+    for (int m = (TPR < 32 ? TPR : 32) / 2; m >= 1; m >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
+    }
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        float2* r = red + slot * W;
+        slot ^= 1;
+        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            v.x += r[w].x;
+            v.y += r[w].y;
+        }
+    }
+    return v;
+}
+
+constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
+
+template <typename IO, int VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArgs p) {
+    constexpr int RPB = norm_block(TPR) / TPR;
+    __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
+    int slot = 0;
+    const int t = threadIdx.x % TPR;
+    const int64_t row0 = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const bool active = row0 < p.rows;
+    const int64_t row = active ? row0 : p.rows - 1;        // idle groups follow along (shuffles)
+    const int cols = (int)p.cols;
+    const IO* x = static_cast<const IO*>(p.x) + row * cols;
+
+    float v[NV * VEC];
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * TPR) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i * VEC + e] = 0.0f;
+        if (c < cols) load_vec<IO, VEC>(x + c, v + i * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s.x += v[i * VEC + e];
+    }
+    float mean = 0.0f;
+    if (!p.rms) mean = row_sum<TPR>(s, red, slot).x * p.inv_cols;
+    s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const bool in = (t + i * TPR) * VEC < cols;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            v[i * VEC + e] -= mean;
+            if (in) s.x = fmaf(v[i * VEC + e], v[i * VEC + e], s.x);
+        }
+    }
+    const float var = row_sum<TPR>(s, red, slot).x * p.inv_cols;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+    if (!active) return;
+    if (t == 0) {
+        if (p.mean && !p.rms) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    IO* y = static_cast<IO*>(p.y) + row * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * TPR) * VEC;
+        if (c >= cols) continue;
+        float w[VEC], b[VEC];
+        load_param<VEC>(p.weight ? p.weight + c : nullptr, w, 1.0f);
+        load_param<VEC>(p.bias ? p.bias + c : nullptr, b, 0.0f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = fmaf(v[i * VEC + e] * rstd, w[e], b[e]);
+        if (p.z) {
+            float z[VEC];
+            load_vec<IO, VEC>(static_cast<const IO*>(p.z) + row * cols + c, z);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] *= z[e] * sigmoid_f32(z[e]);
+        }
+        store_vec<IO, VEC>(y + c, w);
+    }
+}
+
+// Backward.  Rows go to blocks in a grid-stride loop; dw, db of this thread's
+// columns stay in registers over all its rows.
+template <typename IO, int VEC, int TPR, int NV>
+__global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(const NormArgs p) {
+    constexpr int BT = norm_block(TPR);
+    constexpr int RPB = BT / TPR;
+    __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
+    int slot = 0;
+    const int t = threadIdx.x % TPR;
+    const int grp = threadIdx.x / TPR;
+    const int cols = (int)p.cols;
+    float dw[NV * VEC], db[NV * VEC];
+#pragma unroll
+    for (int i = 0; i < NV * VEC; ++i) dw[i] = db[i] = 0.0f;
+
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += (int64_t)gridDim.x * RPB) {
+        const bool active = r0 + grp < p.rows;
+        const int64_t row = active ? r0 + grp : p.rows - 1;
+        const int64_t base = row * cols;
+        const float mean = p.rms ? 0.0f : p.mean[row];
+        const float rstd = p.rstd[row];
+        float xh[NV * VEC], d[NV * VEC];
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * TPR) * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) xh[i * VEC + e] = d[i * VEC + e] = 0.0f;
+            if (c >= cols) continue;
+            load_vec<IO, VEC>(static_cast<const IO*>(p.x) + base + c, xh + i * VEC);
+            load_vec<IO, VEC>(static_cast<const IO*>(p.dy) + base + c, d + i * VEC);
+            float w[VEC];
+            load_param<VEC>(p.weight ? p.weight + c : nullptr, w, 1.0f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) xh[i * VEC + e] = (xh[i * VEC + e] - mean) * rstd;
+            if (p.z) {
+                float z[VEC], b[VEC], dz[VEC];
+                load_vec<IO, VEC>(static_cast<const IO*>(p.z) + base + c, z);
+                load_param<VEC>(p.bias ? p.bias + c : nullptr, b, 0.0f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float sg = sigmoid_f32(z[e]);
+                    const float n = fmaf(xh[i * VEC + e], w[e], b[e]);
+                    dz[e] = d[i * VEC + e] * n * sg * fmaf(z[e], 1.0f - sg, 1.0f);
+                    d[i * VEC + e] *= z[e] * sg;
+                }
+                if (active && p.dz) store_vec<IO, VEC>(static_cast<IO*>(p.dz) + base + c, dz);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int k = i * VEC + e;
+                if (active) {
+                    dw[k] = fmaf(d[k], xh[k], dw[k]);
+                    db[k] += d[k];
+                }
+                d[k] *= w[e];
+                s.x += d[k];
+                s.y = fmaf(d[k], xh[k], s.y);
+            }
+        }
+        s = row_sum<TPR>(s, red, slot);
+        const float a0 = p.rms ? 0.0f : s.x * p.inv_cols;
+        const float a1 = s.y * p.inv_cols;
+        if (active) {
+            IO* dx = static_cast<IO*>(p.dx) + base;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t + i * TPR) * VEC;
+                if (c >= cols) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int k = i * VEC + e;
+                    o[e] = rstd * (d[k] - a0 - xh[k] * a1);
+                }
+                store_vec<IO, VEC>(dx + c, o);
+            }
+        }
+    }
+    if (!p.part) return;
+    // Rows of one block that share a warp: add their sums by shuffles, then
+    // the block's groups in group order through shared memory.
+    float* part = p.part + (int64_t)blockIdx.x * 2 * cols;
+    if constexpr (TPR < 32) {
+#pragma unroll
+        for (int m = TPR; m < 32; m <<= 1)
+#pragma unroll
+            for (int i = 0; i < NV * VEC; ++i) {
+                dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], m);
+                db[i] += __shfl_xor_sync(0xffffffffu, db[i], m);
+            }
+    }
+    if constexpr (RPB > 1) {
+        constexpr int W = BT / 32, TW = TPR < 32 ? TPR : 32;
+        __shared__ float acc[W][TW * NV * VEC];
+        const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (l < TW)
+#pragma unroll
+                for (int i = 0; i < NV * VEC; ++i) acc[w][l * NV * VEC + i] = half ? db[i] : dw[i];
+            __syncthreads();
+            for (int j = threadIdx.x; j < TW * NV * VEC; j += BT) {
+                const int k = j % (NV * VEC);
+                const int c = (j / (NV * VEC) + (k / VEC) * TPR) * VEC + k % VEC;
+                float s = 0.0f;
+#pragma unroll
+                for (int q = 0; q < W; ++q) s += acc[q][j];
+                if (c < cols) part[half * cols + c] = s;
+            }
+            __syncthreads();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * TPR) * VEC;
+            if (c >= cols) continue;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                part[c + e] = dw[i * VEC + e];
+                part[cols + c + e] = db[i * VEC + e];
+            }
+        }
+    }
+}
+
+// dw, db (the two halves of a partial row) = the sums over the blocks, in a
+// fixed order: thread row r adds blocks r, r + 32, ..., then the 32 sums.
+__global__ void __launch_bounds__(1024) norm_param_kernel(const float* part, int nblk, int64_t cols, float* dw, float* db) {
+    __shared__ float acc[32][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float s = 0.0f;
+    if (c < 2 * cols)
+        for (int b = threadIdx.y; b < nblk; b += 32) s += part[(int64_t)b * 2 * cols + c];
+    acc[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < 2 * cols) {
+        s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) s += acc[r][threadIdx.x];
+        if (c < cols) {
+            if (dw) dw[c] = s;
+        } else if (db) {
+            db[c - cols] = s;
+        }
+    }
+}
+
+template <typename IO, int VEC, int TPR, int NV>
+cudaError_t launch_one(const NormArgs& a, bool bwd, cudaStream_t s) {
+    constexpr int BT = norm_block(TPR);
+    constexpr int RPB = BT / TPR;
+    if (!bwd) {
+        const int64_t blocks = (a.rows + RPB - 1) / RPB;
+        if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        norm_fwd_kernel<IO, VEC, TPR, NV><<<(unsigned)blocks, BT, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    norm_bwd_kernel<IO, VEC, TPR, NV><<<(unsigned)norm_bwd_blocks(a.rows, a.cols), BT, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.part) return e;
+    norm_param_kernel<<<(unsigned)((2 * a.cols + 31) / 32), dim3(32, 32), 0, s>>>(
+        a.part, norm_bwd_blocks(a.rows, a.cols), a.cols, a.dweight, a.dbias);
+    return cudaGetLastError();
+}
+
+// Threads of one row: the smallest count whose threads hold it in kElems
+// elements each.
+int norm_tpr(int64_t cols) {
+    return cols <= 8 * kElems ? 8 : cols <= 32 * kElems ? 32 : cols <= 128 * kElems ? 128 : cols <= 512 * kElems ? 512 : 1024;
+}
+
+template <typename IO, int VEC, int TPR>
+cudaError_t launch_tpr(const NormArgs& a, bool bwd, cudaStream_t s) {
+    const int64_t nv = (a.cols + (int64_t)TPR * VEC - 1) / (TPR * VEC);
+    if constexpr (VEC == 1) {
+        if (nv <= 4) return launch_one<IO, VEC, TPR, 4>(a, bwd, s);
+        if (nv <= 8) return launch_one<IO, VEC, TPR, 8>(a, bwd, s);
+        return launch_one<IO, VEC, TPR, 16>(a, bwd, s);
+    } else {
+        if (nv <= 1) return launch_one<IO, VEC, TPR, 1>(a, bwd, s);
+        if (VEC == 8 || nv <= 2) return launch_one<IO, VEC, TPR, 2>(a, bwd, s);
+        return launch_one<IO, VEC, TPR, 16 / VEC>(a, bwd, s);
+    }
+}
+
+template <typename IO, int VEC>
+cudaError_t launch_vec(const NormArgs& a, bool bwd, cudaStream_t s) {
+    switch (norm_tpr(a.cols)) {
+        case 8: return launch_tpr<IO, VEC, 8>(a, bwd, s);
+        case 32: return launch_tpr<IO, VEC, 32>(a, bwd, s);
+        case 128: return launch_tpr<IO, VEC, 128>(a, bwd, s);
+        case 512: return launch_tpr<IO, VEC, 512>(a, bwd, s);
+        default: return launch_tpr<IO, VEC, 1024>(a, bwd, s);
+    }
+}
+
+template <typename IO>
+cudaError_t launch_io(const NormArgs& a, bool bwd, cudaStream_t s) {
+    // Rows of whole 16-byte pieces move 16 bytes at a time, others by element.
+    constexpr int VEC = 16 / sizeof(IO);
+    return a.cols % VEC == 0 ? launch_vec<IO, VEC>(a, bwd, s) : launch_vec<IO, 1>(a, bwd, s);
+}
+
+}  // namespace
+
+// Blocks of the backward: enough to fill 148 SMs at the register use of its
+// threads (about 1024 of them an SM), and no more than there are rows.
+int norm_bwd_blocks(int64_t rows, int64_t cols) {
+    const int tpr = norm_tpr(cols), bt = norm_block(tpr);
+    const int64_t need = (rows + bt / tpr - 1) / (bt / tpr);
+    const int64_t fill = 148 * (1024 / bt);
+    return (int)(need < fill ? need : fill);
+}
+
+cudaError_t launch_norm_fwd(const NormArgs& a, int io, cudaStream_t s) {
+    return io == 0 ? launch_io<float>(a, false, s) : launch_io<bf16>(a, false, s);
+}
+
+cudaError_t launch_norm_bwd(const NormArgs& a, int io, cudaStream_t s) {
+    return io == 0 ? launch_io<float>(a, true, s) : launch_io<bf16>(a, true, s);
+}
+
+}  // namespace mmscan

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <string>
 
+#include "mm_checks.h"
 #include "mm_internal.h"
 
 namespace {
@@ -68,44 +69,14 @@ int64_t seg_len_for(int64_t batch, int64_t L, int64_t dim, int64_t dstate, int i
     return S;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// a * b * ... without int64 overflow; false on overflow.
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > INT64_MAX / a) return false;
-    *out = a * b;
-    return true;
-}
-
-// The kernels form time coordinates of the tiled copies, grid sizes and
-// channel numbers in 32 bits; requests beyond these bounds are refused
-// before launch.
-constexpr int64_t kMaxSeqlen = int64_t(1) << 30;
-constexpr int64_t kMaxIndex = 0x7fffffffLL;
-
-struct Range {
-    const char* name;
-    uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range rng(const char* name, const void* p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, p ? lo + static_cast<uintptr_t>(bytes) : lo};
-}
-
-bool overlap(const Range& a, const Range& b) {
-    if (a.lo == a.hi || b.lo == b.hi) return false;   // NULL / empty
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-// Fault-injection hook for the host-side error path: with
-// MMSCAN_FAULT_INJECT=launch a call that passed its checks returns
-// MM_ERR_CUDA without launching anything.
-bool inject_launch_failure() {
-    const char* v = std::getenv("MMSCAN_FAULT_INJECT");
-    return v && std::strcmp(v, "launch") == 0;
-}
+using mmscan::aligned16;
+using mmscan::inject_launch_failure;
+using mmscan::kMaxIndex;
+using mmscan::kMaxSeqlen;
+using mmscan::mul_ok;
+using mmscan::overlap;
+using mmscan::Range;
+using mmscan::rng;
 
 // Test hook for the device-side give-up path: with MMSCAN_FAULT_INJECT=stall
 // the kernels that stage their inputs through bounded waits (the two forward

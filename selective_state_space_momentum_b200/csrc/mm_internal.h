@@ -205,4 +205,85 @@ unsigned int ssd_mom_tc_read_and_clear_device_error();
 bool ssd_shape_supported(int64_t headdim, int64_t dstate, int64_t chunk);
 cudaError_t launch_ssd_fwd(const SSDArgs& a, cudaStream_t s);
 
+// Gated delta rule (gdr_fwd.cu, gdr_bwd.cu): chunks of kGdrChunk steps.
+constexpr int kGdrChunk = 64;
+constexpr int kGdrRecBytes = 2 * kGdrChunk * kGdrChunk * 2 + 3 * kGdrChunk * 4;   // a chunk's record
+
+// Arguments of one gated-delta-rule call over a sequence (device pointers;
+// sizes as in mm_gdr_dims, bf16 I/O).
+struct GDRArgs {
+    const void* q;         // (batch, L, G, N)
+    const void* k;
+    const void* v;         // (batch, L, H, P)
+    const void* g;         // (batch, L, H)
+    const void* beta;
+    const float* h0;       // (batch, H, P, N) or null
+    void* o;               // (batch, L, H, P)
+    float* hT;             // (batch, H, P, N) or null
+    // per (batch row, head, chunk): the record, the low part of T, and for the
+    // backward the state at the chunk's start (P, N) and the rows written (P, C)
+    void* rec;
+    void* tlo;
+    void* states;          // null: no backward will follow
+    void* u;
+    int64_t batch, seqlen, nheads, ngroups, nchunks;
+    int headdim, dstate;
+    float scale;
+    // backward
+    const void* dout;      // (batch, L, H, P)
+    const float* dhT;      // (batch, H, P, N) or null
+    void* dq;              // (batch, L, G, N)
+    void* dk;
+    void* dv;              // (batch, L, H, P)
+    void* dg;              // (batch, L, H)
+    void* dbeta;
+    float* dh0;            // (batch, H, P, N) or null
+    void* dstates;         // per chunk: the gradient reaching the state at its end (P, N) bf16
+    void* dr;              // per chunk: T^T du (P, C) bf16
+};
+
+// Arguments of one decode step of the gated delta rule.
+struct GDRStepArgs {
+    const void* q;         // (batch, G, N) io
+    const void* k;
+    const void* v;         // (batch, H, P) io
+    const void* g;         // (batch, H) io
+    const void* beta;
+    float* h;              // (batch, H, P, N), read and written
+    void* o;               // (batch, H, P) io
+    int64_t batch, nheads, ngroups;
+    int headdim, dstate;
+    float scale;
+};
+
+bool gdr_shape_supported(int64_t headdim, int64_t dstate);
+cudaError_t launch_gdr_fwd(const GDRArgs& a, cudaStream_t s);
+cudaError_t launch_gdr_bwd(const GDRArgs& a, cudaStream_t s);
+cudaError_t launch_gdr_step(const GDRStepArgs& a, int io, cudaStream_t s);
+
+// Arguments of one layer norm call, forward or backward.
+struct NormArgs {
+    const void* x;         // (rows, cols) io
+    const void* z;         // gate, or null
+    const float* weight;   // (cols) or null
+    const float* bias;
+    const void* dy;
+    void* y;
+    void* dx;
+    void* dz;              // null: not formed
+    float* mean;           // (rows); read by the backward, written by the forward (or null)
+    float* rstd;
+    float* dweight;        // (cols) or null
+    float* dbias;
+    float* part;           // the backward's partial sums, (blocks, 2, cols), or null
+    int64_t rows, cols;
+    float eps, inv_cols;
+    int rms;
+};
+
+constexpr int64_t kNormMaxCols = 16384;
+int norm_bwd_blocks(int64_t rows, int64_t cols);
+cudaError_t launch_norm_fwd(const NormArgs& a, int io, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, int io, cudaStream_t s);
+
 }  // namespace mmscan
