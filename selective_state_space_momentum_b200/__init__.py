@@ -27,6 +27,7 @@ Convenience wrappers allocate outputs:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -205,6 +206,8 @@ def _declare(lib):
 def load_library(path: str | None = None):
     """Load libmmscan.so (raises if it has not been built)."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     if path is not None:
         return _declare(ctypes.CDLL(path))
     with _lock:
@@ -1062,13 +1065,64 @@ def scan_fwd_split_peers(x, delta, A, B, C, seg_len, seqlen_total, peers, h0=Non
 
 
 # ------------------------------------------- gated delta rule, layer norm -----
-# The kernels run on the device that is current when they are launched; these
-# wrappers make the operands' device current for the call, and take that
-# device's current stream by default.
-def _launch(device, stream, call):
+# A decode step or a short prompt runs for a few microseconds on the device,
+# so these wrappers are written for few Python operations a call: an operand
+# that is as it should be passes four comparisons; any other goes to _require
+# for its message.  Workspace sizes are asked of the library once
+# per set of sizes.
+def _operands(items, device, index):
+    """Check (name, tensor, shape, dtype, optional) operands; their pointers."""
+    ptrs = []
+    for name, t, shape, dtype, optional in items:
+        if t is None and optional:
+            ptrs.append(None)
+            continue
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+                ptrs.append(t.data_ptr())
+                continue
+        except AttributeError:
+            pass
+        _require(name, t, shape, (dtype,), device)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _run(index, stream, fn, *args):
+    """fn(*args, stream handle) with the operands' device current: the kernels
+    run on the device that is current when they are launched.  By default on
+    that device's current stream."""
     import torch
-    with torch.cuda.device(device):
-        return call(_stream_handle(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, stream)
+    with torch.cuda.device(index):
+        return fn(*args, stream)
+
+
+def _hold(stream, *tensors):
+    """Tensors a wrapper allocated on the current stream and used on another
+    one: the allocator may hand their memory out again only after that
+    stream's work."""
+    import torch
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _require_bytes(name, t, nbytes, index):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous uint8 tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the operands on cuda:{index}")
+    if t.numel() < nbytes:
+        raise ValueError(f"{name} holds {t.numel()} bytes; the call needs {nbytes}")
+    return t.data_ptr()
 
 
 def _bytes_of(fn, *args) -> int:
@@ -1077,52 +1131,43 @@ def _bytes_of(fn, *args) -> int:
     return int(out.value)
 
 
-def _require_bytes(name, t, nbytes, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous uint8 tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the operands on {device}")
-    if t.numel() < nbytes:
-        raise ValueError(f"{name} holds {t.numel()} bytes; the call needs {nbytes}")
-
-
-def _gdr_dims(q, k, v, g, beta, tensors, step=False):
-    """v (batch[, L], H, P) and q (batch[, L], G, N) fix the sizes; `tensors`
-    is a list of (name, tensor, kind, optional), kind v, qk, gate or state."""
-    import torch
-    load_library()
-    dev, io = _lead(v, 3 if step else 4, "v")
-    if not step and io != torch.bfloat16:
-        raise TypeError("the gated delta rule over a sequence takes bf16 q, k, v, g, beta and o")
-    if not isinstance(q, torch.Tensor) or q.dim() != v.dim():
-        raise ValueError(f"q must be a {v.dim()}-D tensor like v")
-    lead, (H, P), (G, N) = tuple(v.shape[:-2]), v.shape[-2:], q.shape[-2:]
-    shapes = {"qk": (lead + (G, N), (io,)), "v": (lead + (H, P), (io,)), "gate": (lead + (H,), (io,)),
-              "state": ((v.shape[0], H, P, N), (torch.float32,))}
-    for name, t, kind, optional in [("q", q, "qk", False), ("k", k, "qk", False), ("g", g, "gate", False),
-                                    ("beta", beta, "gate", False)] + tensors:
-        shape, dts = shapes[kind]
-        _require(name, t, shape, dts, dev, optional)
-    _on_cuda(dev)
-    return GDRDims(v.shape[0], 1 if step else v.shape[1], H, P, N, G, _io_code(io))
-
-
+@functools.lru_cache(maxsize=1024)
 def mm_gdr_fwd_workspace_size(batch, seqlen, nheads, headdim, dstate, ngroups, with_ckpt=False) -> int:
     """C entry point mm_gdr_fwd_workspace_size: bytes of mm_gdr_fwd's workspace."""
     dims = GDRDims(batch, seqlen, nheads, headdim, dstate, ngroups, MM_BF16)
     return _bytes_of("mm_gdr_fwd_workspace_size", ctypes.byref(dims), 1 if with_ckpt else 0)
 
 
+@functools.lru_cache(maxsize=1024)
 def mm_gdr_ckpt_size(batch, seqlen, nheads, headdim, dstate, ngroups) -> int:
     """C entry point mm_gdr_ckpt_size: bytes of the buffer mm_gdr_bwd restarts from."""
     return _bytes_of("mm_gdr_ckpt_size", ctypes.byref(GDRDims(batch, seqlen, nheads, headdim, dstate, ngroups, MM_BF16)))
 
 
+@functools.lru_cache(maxsize=1024)
 def mm_gdr_bwd_workspace_size(batch, seqlen, nheads, headdim, dstate, ngroups) -> int:
     """C entry point mm_gdr_bwd_workspace_size: bytes of mm_gdr_bwd's workspace."""
     return _bytes_of("mm_gdr_bwd_workspace_size",
                      ctypes.byref(GDRDims(batch, seqlen, nheads, headdim, dstate, ngroups, MM_BF16)))
+
+
+def _gdr_sizes(q, v, ndim=4):
+    """(batch, L, H, P, N, G) of a call, from v (batch[, L], H, P) and q (batch[, L], G, N)."""
+    import torch
+    load_library()
+    for name, t in (("v", v), ("q", q)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    if v.dtype is not torch.bfloat16 and (ndim == 4 or v.dtype is not torch.float32):
+        raise TypeError("the gated delta rule takes bf16 q, k, v, g, beta and o over a sequence, bf16 or fp32 for a "
+                        f"step (got {v.dtype})")
+    if ndim == 3:
+        (B, H, P), (G, N), L = v.shape, q.shape[1:], 1
+    else:
+        (B, L, H, P), (G, N) = v.shape, q.shape[2:]
+    return B, L, H, P, N, G
 
 
 def mm_gdr_fwd(q, k, v, g, beta, h0, scale, o, hT, ckpt, workspace, stream=None):
@@ -1132,28 +1177,46 @@ def mm_gdr_fwd(q, k, v, g, beta, h0, scale, o, hT, ckpt, workspace, stream=None)
     h0, hT (batch, H, P, N) fp32 or None; ckpt (mm_gdr_ckpt_size bytes, or
     None) and workspace (mm_gdr_fwd_workspace_size bytes) uint8.
     """
-    dims = _gdr_dims(q, k, v, g, beta, [("h0", h0, "state", True), ("o", o, "v", False), ("hT", hT, "state", True)])
-    ref, lib = ctypes.byref(dims), load_library()
-    if ckpt is not None:
-        _require_bytes("ckpt", ckpt, _bytes_of("mm_gdr_ckpt_size", ref), v.device)
-    _require_bytes("workspace", workspace, _bytes_of("mm_gdr_fwd_workspace_size", ref, 0 if ckpt is None else 1), v.device)
-    _check(_launch(v.device, stream, lambda s: lib.mm_gdr_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), float(scale), _ptr(o), _ptr(hT), _ptr(ckpt),
-        _ptr(workspace), workspace.numel(), ref, s)), "mm_gdr_fwd")
+    _gdr_fwd(_gdr_sizes(q, v), q, k, v, g, beta, h0, scale, o, hT, ckpt, workspace, stream)
+
+
+def _gdr_fwd(sizes, q, k, v, g, beta, h0, scale, o, hT, ckpt, workspace, stream):
+    import torch
+    B, L, H, P, N, G = sizes
+    io, f32, dev, index = v.dtype, torch.float32, v.device, v.get_device()
+    qk, vs, gate, state = (B, L, G, N), (B, L, H, P), (B, L, H), (B, H, P, N)
+    ptrs = _operands((("q", q, qk, io, False), ("k", k, qk, io, False), ("v", v, vs, io, False), ("g", g, gate, io, False),
+                      ("beta", beta, gate, io, False), ("h0", h0, state, f32, True), ("o", o, vs, io, False),
+                      ("hT", hT, state, f32, True)), dev, index)
+    if index < 0:
+        _on_cuda(dev)
+    ck = None if ckpt is None else _require_bytes("ckpt", ckpt, mm_gdr_ckpt_size(*sizes), index)
+    ws = _require_bytes("workspace", workspace, mm_gdr_fwd_workspace_size(*sizes, ckpt is not None), index)
+    _check(_run(index, stream, load_library().mm_gdr_fwd, *ptrs[:6], scale, *ptrs[6:], ck, ws, workspace.numel(),
+                ctypes.byref(GDRDims(B, L, H, P, N, G, MM_BF16))), "mm_gdr_fwd")
 
 
 def mm_gdr_bwd(q, k, v, g, beta, scale, ckpt, dout, dhT, dq, dk, dv, dg, dbeta, dh0, workspace, stream=None):
     """C entry point mm_gdr_bwd on torch CUDA tensors (marshalling only): the
     gradients have the shapes and types of q, k, v, g, beta and h0."""
-    dims = _gdr_dims(q, k, v, g, beta, [("dout", dout, "v", False), ("dhT", dhT, "state", True), ("dq", dq, "qk", False),
-                                        ("dk", dk, "qk", False), ("dv", dv, "v", False), ("dg", dg, "gate", False),
-                                        ("dbeta", dbeta, "gate", False), ("dh0", dh0, "state", True)])
-    ref, lib = ctypes.byref(dims), load_library()
-    _require_bytes("ckpt", ckpt, _bytes_of("mm_gdr_ckpt_size", ref), v.device)
-    _require_bytes("workspace", workspace, _bytes_of("mm_gdr_bwd_workspace_size", ref), v.device)
-    _check(_launch(v.device, stream, lambda s: lib.mm_gdr_bwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(ckpt), _ptr(dout), _ptr(dhT), _ptr(dq), _ptr(dk),
-        _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), _ptr(workspace), workspace.numel(), ref, s)), "mm_gdr_bwd")
+    _gdr_bwd(_gdr_sizes(q, v), q, k, v, g, beta, scale, ckpt, dout, dhT, dq, dk, dv, dg, dbeta, dh0, workspace, stream)
+
+
+def _gdr_bwd(sizes, q, k, v, g, beta, scale, ckpt, dout, dhT, dq, dk, dv, dg, dbeta, dh0, workspace, stream):
+    import torch
+    B, L, H, P, N, G = sizes
+    io, f32, dev, index = v.dtype, torch.float32, v.device, v.get_device()
+    qk, vs, gate, state = (B, L, G, N), (B, L, H, P), (B, L, H), (B, H, P, N)
+    ptrs = _operands((("q", q, qk, io, False), ("k", k, qk, io, False), ("v", v, vs, io, False), ("g", g, gate, io, False),
+                      ("beta", beta, gate, io, False), ("dout", dout, vs, io, False), ("dhT", dhT, state, f32, True),
+                      ("dq", dq, qk, io, False), ("dk", dk, qk, io, False), ("dv", dv, vs, io, False),
+                      ("dg", dg, gate, io, False), ("dbeta", dbeta, gate, io, False), ("dh0", dh0, state, f32, True)), dev, index)
+    if index < 0:
+        _on_cuda(dev)
+    ck = _require_bytes("ckpt", ckpt, mm_gdr_ckpt_size(*sizes), index)
+    ws = _require_bytes("workspace", workspace, mm_gdr_bwd_workspace_size(*sizes), index)
+    _check(_run(index, stream, load_library().mm_gdr_bwd, *ptrs[:5], scale, ck, *ptrs[5:], ws, workspace.numel(),
+                ctypes.byref(GDRDims(B, L, H, P, N, G, MM_BF16))), "mm_gdr_bwd")
 
 
 def mm_gdr_step(q, k, v, g, beta, h, scale, o, stream=None):
@@ -1162,39 +1225,52 @@ def mm_gdr_step(q, k, v, g, beta, h, scale, o, stream=None):
     q, k (batch, G, N), v, o (batch, H, P), g, beta (batch, H) in one storage
     type (fp32 or bf16); h (batch, H, P, N) fp32, updated in place.
     """
-    dims = _gdr_dims(q, k, v, g, beta, [("h", h, "state", False), ("o", o, "v", False)], step=True)
-    lib = load_library()
-    _check(_launch(v.device, stream, lambda s: lib.mm_gdr_step(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h), float(scale), _ptr(o), ctypes.byref(dims), s)), "mm_gdr_step")
+    _gdr_step(_gdr_sizes(q, v, 3), q, k, v, g, beta, h, scale, o, stream)
 
 
-def _gdr_outputs(v, q, return_last_state, with_ckpt):
+def _gdr_step(sizes, q, k, v, g, beta, h, scale, o, stream):
     import torch
-    if not isinstance(v, torch.Tensor) or v.dim() != 4 or not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q and v must be 4-D (batch, L, heads, width) tensors")
-    sizes = (v.shape[0], v.shape[1], v.shape[2], v.shape[3], q.shape[3], q.shape[2])
-    dev = v.device
-    hT = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), device=dev, dtype=torch.float32) if return_last_state else None
-    ckpt = torch.empty(mm_gdr_ckpt_size(*sizes), device=dev, dtype=torch.uint8) if with_ckpt else None
-    return torch.empty_like(v), hT, ckpt, torch.empty(mm_gdr_fwd_workspace_size(*sizes, with_ckpt), device=dev, dtype=torch.uint8)
+    B, L, H, P, N, G = sizes
+    io, dev, index = v.dtype, v.device, v.get_device()
+    qk, vs, gate = (B, G, N), (B, H, P), (B, H)
+    ptrs = _operands((("q", q, qk, io, False), ("k", k, qk, io, False), ("v", v, vs, io, False), ("g", g, gate, io, False),
+                      ("beta", beta, gate, io, False), ("h", h, (B, H, P, N), torch.float32, False), ("o", o, vs, io, False)),
+                     dev, index)
+    if index < 0:
+        _on_cuda(dev)
+    _check(_run(index, stream, load_library().mm_gdr_step, *ptrs[:6], scale, ptrs[6],
+                ctypes.byref(GDRDims(B, 1, H, P, N, G, MM_F32 if io is torch.float32 else MM_BF16))), "mm_gdr_step")
 
 
 def gdr_fwd(q, k, v, g, beta, h0=None, scale=None, return_last_state=True, stream=None):
     """The gated delta rule over a sequence: allocate outputs and workspace and
     run mm_gdr_fwd; returns (o, hT) (hT None when ``return_last_state`` is
     False).  scale: 1 / sqrt(N) by default."""
-    o, hT, _, ws = _gdr_outputs(v, q, return_last_state, False)
-    mm_gdr_fwd(q, k, v, g, beta, h0, q.shape[3] ** -0.5 if scale is None else scale, o, hT, None, ws, stream)
-    _hold(stream, o, hT, ws)
+    import torch
+    sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
+    dev = v.device
+    o = torch.empty_like(v)
+    hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
+    ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, False), device=dev, dtype=torch.uint8)
+    _gdr_fwd(sizes, q, k, v, g, beta, h0, N ** -0.5 if scale is None else scale, o, hT, None, ws, stream)
+    if stream is not None:
+        _hold(stream, o, hT, ws)
     return o, hT
 
 
 def gdr_fwd_train(q, k, v, g, beta, h0=None, scale=None, return_last_state=False, stream=None):
     """gdr_fwd that also keeps what the backward needs: returns (o, hT, ckpt),
     ckpt uint8 (hT None unless ``return_last_state``)."""
-    o, hT, ckpt, ws = _gdr_outputs(v, q, return_last_state, True)
-    mm_gdr_fwd(q, k, v, g, beta, h0, q.shape[3] ** -0.5 if scale is None else scale, o, hT, ckpt, ws, stream)
-    _hold(stream, o, hT, ckpt, ws)
+    import torch
+    sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
+    dev = v.device
+    o = torch.empty_like(v)
+    hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
+    ckpt = torch.empty(mm_gdr_ckpt_size(*sizes), device=dev, dtype=torch.uint8)
+    ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, True), device=dev, dtype=torch.uint8)
+    _gdr_fwd(sizes, q, k, v, g, beta, h0, N ** -0.5 if scale is None else scale, o, hT, ckpt, ws, stream)
+    if stream is not None:
+        _hold(stream, o, hT, ckpt, ws)
     return o, hT, ckpt
 
 
@@ -1202,17 +1278,17 @@ def gdr_bwd(q, k, v, g, beta, ckpt, dout, dhT=None, scale=None, return_dh0=False
     """Allocate the gradients and run mm_gdr_bwd; returns a dict with dq, dk,
     dv, dg, dbeta and, with ``return_dh0``, dh0."""
     import torch
-    if not isinstance(v, torch.Tensor) or v.dim() != 4 or not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q and v must be 4-D (batch, L, heads, width) tensors")
-    sizes = (v.shape[0], v.shape[1], v.shape[2], v.shape[3], q.shape[3], q.shape[2])
-    grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
-             "dbeta": torch.empty_like(beta)}
-    dh0 = torch.empty((v.shape[0], v.shape[2], v.shape[3], q.shape[3]), device=v.device, dtype=torch.float32) if return_dh0 else None
+    sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
+    grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
+             "dg": torch.empty((B, L, H), device=v.device, dtype=v.dtype),
+             "dbeta": torch.empty((B, L, H), device=v.device, dtype=v.dtype)}
+    dh0 = torch.empty((B, H, P, N), device=v.device, dtype=torch.float32) if return_dh0 else None
     ws = torch.empty(mm_gdr_bwd_workspace_size(*sizes), device=v.device, dtype=torch.uint8)
-    mm_gdr_bwd(q, k, v, g, beta, q.shape[3] ** -0.5 if scale is None else scale, ckpt, dout, dhT, *grads.values(), dh0, ws, stream)
+    _gdr_bwd(sizes, q, k, v, g, beta, N ** -0.5 if scale is None else scale, ckpt, dout, dhT, *grads.values(), dh0, ws, stream)
     if return_dh0:
         grads["dh0"] = dh0
-    _hold(stream, ws, *grads.values())
+    if stream is not None:
+        _hold(stream, ws, *grads.values())
     return grads
 
 
@@ -1220,56 +1296,49 @@ def gdr_step(q, k, v, g, beta, h, scale=None, stream=None):
     """One decode step of the gated delta rule: h (batch, H, P, N) fp32 is
     updated in place; returns o (batch, H, P)."""
     import torch
-    if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q and v must be 3-D (batch, heads, width) tensors")
+    sizes = _gdr_sizes(q, v, 3)
     o = torch.empty_like(v)
-    mm_gdr_step(q, k, v, g, beta, h, q.shape[2] ** -0.5 if scale is None else scale, o, stream)
-    _hold(stream, o)
+    _gdr_step(sizes, q, k, v, g, beta, h, sizes[4] ** -0.5 if scale is None else scale, o, stream)
+    if stream is not None:
+        _hold(stream, o)
     return o
 
 
-def _hold(stream, *tensors):
-    """Tensors a wrapper allocated on the current stream and used on another
-    one: the allocator may hand their memory out again only after that
-    stream's work."""
-    import torch
-    if stream is None:
-        return
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
-
-
-def _norm_dims(x, weight, bias, z, tensors):
-    """x (..., cols) fixes the sizes; rows are its leading dimensions together."""
+def _norm_dims(x):
+    """(rows, cols) of x (..., cols): rows are its leading dimensions together."""
     import torch
     load_library()
-    if not isinstance(x, torch.Tensor) or x.dim() < 1:
-        raise TypeError("x must be a torch.Tensor with at least one dimension")
-    dev, io = _lead(x, x.dim())
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"x must be a torch.Tensor, got {type(x).__name__}")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        _io_code(x.dtype)
     cols = x.shape[-1]
-    rows = x.numel() // cols if cols else 0
-    f32 = (torch.float32,)
-    shapes = {"io": (tuple(x.shape), (io,)), "col": ((cols,), f32), "row": (tuple(x.shape[:-1]), f32)}
-    for name, t, kind, optional in [("weight", weight, "col", True), ("bias", bias, "col", True), ("z", z, "io", True)] + tensors:
-        shape, dts = shapes[kind]
-        _require(name, t, shape, dts, dev, optional)
-    _on_cuda(dev)
-    return NormDims(rows, cols, _io_code(io))
+    return (x.numel() // cols if cols else 0), cols
 
 
 def mm_layer_norm_fwd(x, weight, bias, z, eps, rms, y, mean, rstd, stream=None):
     """C entry point mm_layer_norm_fwd on torch CUDA tensors (marshalling
     only): x, z, y (..., cols) in one storage type, weight, bias (cols,) fp32,
     mean, rstd (...) fp32; weight, bias, z, mean, rstd may be None."""
-    dims = _norm_dims(x, weight, bias, z, [("y", y, "io", False), ("mean", mean, "row", True), ("rstd", rstd, "row", True)])
-    lib = load_library()
-    _check(_launch(x.device, stream, lambda s: lib.mm_layer_norm_fwd(
-        _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), float(eps), 1 if rms else 0, _ptr(y), _ptr(mean), _ptr(rstd),
-        ctypes.byref(dims), s)), "mm_layer_norm_fwd")
+    _norm_fwd(_norm_dims(x), x, weight, bias, z, eps, rms, y, mean, rstd, stream)
 
 
+def _norm_fwd(sizes, x, weight, bias, z, eps, rms, y, mean, rstd, stream):
+    import torch
+    rows, cols = sizes
+    io, f32, dev, index, full, row = x.dtype, torch.float32, x.device, x.get_device(), x.shape, x.shape[:-1]
+    ptrs = _operands((("x", x, full, io, False), ("weight", weight, (cols,), f32, True), ("bias", bias, (cols,), f32, True),
+                      ("z", z, full, io, True), ("y", y, full, io, False), ("mean", mean, row, f32, True),
+                      ("rstd", rstd, row, f32, True)), dev, index)
+    if index < 0:
+        _on_cuda(dev)
+    _check(_run(index, stream, load_library().mm_layer_norm_fwd, *ptrs[:4], eps, 1 if rms else 0, *ptrs[4:],
+                ctypes.byref(NormDims(rows, cols, MM_F32 if io is f32 else MM_BF16))), "mm_layer_norm_fwd")
+
+
+@functools.lru_cache(maxsize=1024)
 def mm_layer_norm_bwd_workspace_size(rows, cols, io=MM_F32) -> int:
     """C entry point mm_layer_norm_bwd_workspace_size."""
     return _bytes_of("mm_layer_norm_bwd_workspace_size", ctypes.byref(NormDims(rows, cols, io)))
@@ -1279,28 +1348,38 @@ def mm_layer_norm_bwd(x, weight, bias, z, rms, mean, rstd, dy, dx, dweight, dbia
     """C entry point mm_layer_norm_bwd (marshalling only): dx, dz like x,
     dweight, dbias (cols,) fp32 or None, workspace uint8 (None when neither
     dweight nor dbias is asked for)."""
-    dims = _norm_dims(x, weight, bias, z, [("mean", mean, "row", bool(rms)), ("rstd", rstd, "row", False), ("dy", dy, "io", False),
-                                           ("dx", dx, "io", False), ("dweight", dweight, "col", True),
-                                           ("dbias", dbias, "col", True), ("dz", dz, "io", True)])
-    ref, lib = ctypes.byref(dims), load_library()
+    _norm_bwd(_norm_dims(x), x, weight, bias, z, rms, mean, rstd, dy, dx, dweight, dbias, dz, workspace, stream)
+
+
+def _norm_bwd(sizes, x, weight, bias, z, rms, mean, rstd, dy, dx, dweight, dbias, dz, workspace, stream):
+    import torch
+    rows, cols = sizes
+    io, f32, dev, index, full, row = x.dtype, torch.float32, x.device, x.get_device(), x.shape, x.shape[:-1]
+    ptrs = _operands((("x", x, full, io, False), ("weight", weight, (cols,), f32, True), ("bias", bias, (cols,), f32, True),
+                      ("z", z, full, io, True), ("mean", mean, row, f32, bool(rms)), ("rstd", rstd, row, f32, False),
+                      ("dy", dy, full, io, False), ("dx", dx, full, io, False), ("dweight", dweight, (cols,), f32, True),
+                      ("dbias", dbias, (cols,), f32, True), ("dz", dz, full, io, True)), dev, index)
+    if index < 0:
+        _on_cuda(dev)
+    ws, have = None, 0
     if dweight is not None or dbias is not None:
-        _require_bytes("workspace", workspace, _bytes_of("mm_layer_norm_bwd_workspace_size", ref), x.device)
-    _check(_launch(x.device, stream, lambda s: lib.mm_layer_norm_bwd(
-        _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), 1 if rms else 0, _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dweight),
-        _ptr(dbias), _ptr(dz), _ptr(workspace), 0 if workspace is None else workspace.numel(), ref, s)), "mm_layer_norm_bwd")
+        ws = _require_bytes("workspace", workspace, mm_layer_norm_bwd_workspace_size(rows, cols, _io_code(io)), index)
+        have = workspace.numel()
+    _check(_run(index, stream, load_library().mm_layer_norm_bwd, *ptrs[:4], 1 if rms else 0, *ptrs[4:], ws, have,
+                ctypes.byref(NormDims(rows, cols, MM_F32 if io is f32 else MM_BF16))), "mm_layer_norm_bwd")
 
 
 def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, stream=None):
     """Layer norm over the last dimension of x (RMS norm with ``rms``), gated
     by silu(z) when z is given: returns (y, mean, rstd), mean None with rms."""
     import torch
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"x must be a torch.Tensor, got {type(x).__name__}")
+    sizes = _norm_dims(x)
     y = torch.empty_like(x)
-    rstd = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
     mean = None if rms else torch.empty_like(rstd)
-    mm_layer_norm_fwd(x, weight, bias, z, eps, rms, y, mean, rstd, stream)
-    _hold(stream, y, mean, rstd)
+    _norm_fwd(sizes, x, weight, bias, z, eps, rms, y, mean, rstd, stream)
+    if stream is not None:
+        _hold(stream, y, mean, rstd)
     return y, mean, rstd
 
 
@@ -1308,17 +1387,18 @@ def layer_norm_bwd(x, weight, bias, mean, rstd, dy, z=None, rms=False, stream=No
     """Allocate the gradients and run mm_layer_norm_bwd: returns a dict with
     dx and, for each that was given, dweight, dbias, dz."""
     import torch
-    if not isinstance(x, torch.Tensor) or x.dim() < 1:
-        raise TypeError("x must be a torch.Tensor with at least one dimension")
+    sizes = rows, cols = _norm_dims(x)
     grads = {"dx": torch.empty_like(x)}
-    for name, t in (("dweight", weight), ("dbias", bias), ("dz", z)):
-        if t is not None:
-            grads[name] = torch.empty_like(t)
     ws = None
     if weight is not None or bias is not None:
-        cols = max(1, x.shape[-1])
-        ws = torch.empty(mm_layer_norm_bwd_workspace_size(x.numel() // cols, cols, _io_code(x.dtype)), device=x.device, dtype=torch.uint8)
-    mm_layer_norm_bwd(x, weight, bias, z, rms, mean, rstd, dy, grads["dx"], grads.get("dweight"), grads.get("dbias"), grads.get("dz"),
-                      ws, stream)
-    _hold(stream, ws, *grads.values())
+        ws = torch.empty(mm_layer_norm_bwd_workspace_size(rows, cols, _io_code(x.dtype)), device=x.device, dtype=torch.uint8)
+        for name, t in (("dweight", weight), ("dbias", bias)):
+            if t is not None:
+                grads[name] = torch.empty((cols,), device=x.device, dtype=torch.float32)
+    if z is not None:
+        grads["dz"] = torch.empty_like(x)
+    _norm_bwd(sizes, x, weight, bias, z, rms, mean, rstd, dy, grads["dx"], grads.get("dweight"), grads.get("dbias"),
+              grads.get("dz"), ws, stream)
+    if stream is not None:
+        _hold(stream, ws, *grads.values())
     return grads

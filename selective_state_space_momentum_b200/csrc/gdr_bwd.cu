@@ -19,11 +19,10 @@
 //     dg_t  = sum_{i >= t} dc_i over the chunk
 // (the diagonal of W would cancel between its row and its column).
 //
-// Two launches: gdr_bwd_chain_kernel walks the chunks backwards, one warp per
-// 16 rows p of dS as in the forward, and writes dv, r and dS' per chunk;
-// gdr_bwd_grad_kernel, parallel over chunks, forms the rest.  dq and dk of a
-// group sum over its heads inside one block: no atomics, the same bits in
-// every run.
+// Two launches: gdr_chain_kernel (gdr_chain.cu) walks the chunks backwards and
+// writes dv, r and dS' per chunk; gdr_bwd_grad_kernel, parallel over chunks,
+// forms the rest.  dq and dk of a group sum over its heads inside one block:
+// no atomics, the same bits in every run.
 //
 // Precision: every gradient leaves as bf16 (2^-9).  The operands of the
 // products are rounded to bf16 once each; products, sums, dS, the row sums
@@ -33,206 +32,6 @@
 namespace mmscan {
 
 namespace gdr {
-
-template <int DK, int NW>
-struct BwdChainSmem {
-    static constexpr int K = 0, Q = C * DK * 2, T = 2 * C * DK * 2, PM = T + C * C * 2;
-    static constexpr int V = PM + C * C * 2, VB = 32 * NW;
-    static constexpr int F = V + C * VB, STAGE = F + 1024;
-    static constexpr int BYTES = 2 * STAGE;
-    static_assert(VB == 128 || VB == 256, "a row of dO is a tile row");
-};
-
-template <int DK, int NW>
-__global__ void __launch_bounds__(32 * NW, 1) gdr_bwd_chain_kernel(const GDRArgs p) {
-    using L = BwdChainSmem<DK, NW>;
-    constexpr int RB = DK * 2, VB = L::VB, NT = DK / 8, DVT = 16 * NW, NTH = 32 * NW;
-    extern __shared__ __align__(1024) unsigned char sm[];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int gq = lane >> 2, tq = lane & 3;
-    const int tiles = p.headdim / DVT;
-    const int64_t bh = blockIdx.x / tiles;
-    const int p0 = (int)(blockIdx.x % tiles) * DVT;
-    const int64_t b = bh / p.nheads, h = bh - b * p.nheads;
-    const int64_t kstride = p.ngroups * DK * 2, vstride = p.nheads * p.headdim * 2;
-    const unsigned char* kg = static_cast<const unsigned char*>(p.k) + b * p.seqlen * kstride + h / (p.nheads / p.ngroups) * DK * 2;
-    const unsigned char* qg = static_cast<const unsigned char*>(p.q) + b * p.seqlen * kstride + h / (p.nheads / p.ngroups) * DK * 2;
-    const int64_t voff = b * p.seqlen * vstride + (h * p.headdim + p0) * 2;
-    const unsigned char* og = static_cast<const unsigned char*>(p.dout) + voff;
-
-    auto issue = [&](int64_t ch) {
-        unsigned char* st = sm + (ch & 1) * L::STAGE;
-        const int64_t t0 = ch * C;
-        const int valid = (int)(p.seqlen - t0 < C ? p.seqlen - t0 : C);
-        const unsigned char* rg = static_cast<const unsigned char*>(p.rec) + (bh * p.nchunks + ch) * REC_BYTES;
-        load_tile<RB, C>(st + L::K, kg + t0 * kstride, kstride, valid, tid, NTH);
-        load_tile<RB, C>(st + L::Q, qg + t0 * kstride, kstride, valid, tid, NTH);
-        load_tile<128, C>(st + L::T, rg + REC_T, 128, C, tid, NTH);
-        load_tile<128, C>(st + L::PM, rg + REC_P, 128, C, tid, NTH);
-        load_tile<VB, C>(st + L::V, og + t0 * vstride, vstride, valid, tid, NTH);
-        if (tid < 48) cp_async_16(st + L::F + tid * 16, rg + REC_F + tid * 16, 16);
-        cp_async_commit();
-    };
-
-    const int64_t prow = bh * p.headdim + p0 + 16 * w + gq;
-    float s[NT][4];                          // dS^T of this warp's rows p
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float2 x = f2(0.0f, 0.0f), y = x;
-        if (p.dhT) {
-            x = *reinterpret_cast<const float2*>(p.dhT + prow * DK + 8 * n + 2 * tq);
-            y = *reinterpret_cast<const float2*>(p.dhT + (prow + 8) * DK + 8 * n + 2 * tq);
-        }
-        s[n][0] = x.x; s[n][1] = x.y; s[n][2] = y.x; s[n][3] = y.y;
-    }
-    issue(p.nchunks - 1);
-    for (int64_t ch = p.nchunks - 1; ch >= 0; --ch) {
-        cp_async_wait<0>();
-        __syncthreads();
-        if (ch > 0) issue(ch - 1);
-        unsigned char* st = sm + (ch & 1) * L::STAGE;
-        const uint32_t ks = smem_u32(st + L::K), qs = smem_u32(st + L::Q), ts = smem_u32(st + L::T),
-                       ps = smem_u32(st + L::PM), vs = smem_u32(st + L::V);
-        const float* eg = reinterpret_cast<const float*>(st + L::F);
-        const int64_t rec = bh * p.nchunks + ch;
-
-        bf16* sv = static_cast<bf16*>(p.dstates) + (rec * p.headdim + p0 + 16 * w + gq) * DK + 2 * tq;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<uint32_t*>(sv + 8 * n) = pack_bf16x2(s[n][0], s[n][1]);
-            *reinterpret_cast<uint32_t*>(sv + 8 * DK + 8 * n) = pack_bf16x2(s[n][2], s[n][3]);
-        }
-        // x = tail (dS' k) + do Pm
-        float x[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[n][e] = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt) {
-            uint32_t a[4];
-            acc_to_a<NT>(s, kt, a);
-#pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-                uint32_t f[4];
-                load_b_nk<RB>(ks, 8 * n, 2 * kt, lane, f);
-                mma(x[n], a, f[0], f[1]);
-                mma(x[n + 1], a, f[2], f[3]);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float2 t = *reinterpret_cast<const float2*>(eg + C + 8 * n + 2 * tq);
-            x[n][0] *= t.x; x[n][1] *= t.y; x[n][2] *= t.x; x[n][3] *= t.y;
-        }
-        uint32_t dof[4][4];
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            load_a_km<VB>(vs, 16 * kt, 2 * w, lane, dof[kt]);
-#pragma unroll
-            for (int n = 0; n <= 2 * kt; n += 2) {
-                uint32_t f[4];
-                load_b_kn<128>(ps, 16 * kt, n, lane, f);
-                mma(x[n], dof[kt], f[0], f[1]);
-                mma(x[n + 1], dof[kt], f[2], f[3]);
-            }
-        }
-        // r = x T
-        float r[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) r[n][e] = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t a[4];
-            acc_to_a<8>(x, kt, a);
-#pragma unroll
-            for (int n = 0; n <= 2 * kt; n += 2) {
-                uint32_t f[4];
-                load_b_kn<128>(ts, 16 * kt, n, lane, f);
-                mma(r[n], a, f[0], f[1]);
-                mma(r[n + 1], a, f[2], f[3]);
-            }
-        }
-        bf16* rv = static_cast<bf16*>(p.dr) + (rec * p.headdim + p0 + 16 * w + gq) * C + 2 * tq;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            *reinterpret_cast<uint32_t*>(rv + 8 * n) = pack_bf16x2(r[n][0], r[n][1]);
-            *reinterpret_cast<uint32_t*>(rv + 8 * C + 8 * n) = pack_bf16x2(r[n][2], r[n][3]);
-        }
-        // dS <- e^(c_last) dS' + (scale e^c do) q - (beta e^c r) k
-        const float last = eg[C - 1];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] *= last;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            const float2 e0 = *reinterpret_cast<const float2*>(eg + 16 * kt + 2 * tq);
-            const float2 e1 = *reinterpret_cast<const float2*>(eg + 16 * kt + 8 + 2 * tq);
-            uint32_t a[4];
-            a[0] = pack_bf16x2(bf16_lo(dof[kt][0]) * (e0.x * p.scale), bf16_hi(dof[kt][0]) * (e0.y * p.scale));
-            a[1] = pack_bf16x2(bf16_lo(dof[kt][1]) * (e0.x * p.scale), bf16_hi(dof[kt][1]) * (e0.y * p.scale));
-            a[2] = pack_bf16x2(bf16_lo(dof[kt][2]) * (e1.x * p.scale), bf16_hi(dof[kt][2]) * (e1.y * p.scale));
-            a[3] = pack_bf16x2(bf16_lo(dof[kt][3]) * (e1.x * p.scale), bf16_hi(dof[kt][3]) * (e1.y * p.scale));
-#pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t f[4];
-                load_b_kn<RB>(qs, 16 * kt, n, lane, f);
-                mma(s[n], a, f[0], f[1]);
-                mma(s[n + 1], a, f[2], f[3]);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float2 be = *reinterpret_cast<const float2*>(eg + 2 * C + 8 * n + 2 * tq);
-            r[n][0] *= be.x; r[n][1] *= be.y; r[n][2] *= be.x; r[n][3] *= be.y;      // dv
-        }
-        // dv through the warp's own columns of dO's tile (read above) to memory
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-            const int m = lane >> 3;
-            stsm4t(vs + tile_off<VB>(8 * n + (m >> 1) * 8 + (lane & 7), 2 * w + (m & 1)), pack_bf16x2(r[n][0], r[n][1]),
-                   pack_bf16x2(r[n][2], r[n][3]), pack_bf16x2(r[n + 1][0], r[n + 1][1]), pack_bf16x2(r[n + 1][2], r[n + 1][3]));
-        }
-        __syncwarp();
-        const int valid = (int)(p.seqlen - ch * C < C ? p.seqlen - ch * C : C);
-        unsigned char* dvg = static_cast<unsigned char*>(p.dv) + voff + ch * C * vstride + 32 * w;
-#pragma unroll
-        for (int i = lane; i < 2 * C; i += 32) {
-            const int row = i >> 1, c = i & 1;
-            if (row < valid)
-                *reinterpret_cast<uint4*>(dvg + row * vstride + c * 16) =
-                    *reinterpret_cast<const uint4*>(st + L::V + tile_off<VB>(row, 2 * w + c));
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float2 e = *reinterpret_cast<const float2*>(eg + 8 * n + 2 * tq);
-            r[n][0] *= -e.x; r[n][1] *= -e.y; r[n][2] *= -e.x; r[n][3] *= -e.y;
-        }
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t a[4];
-            acc_to_a<8>(r, kt, a);
-#pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t f[4];
-                load_b_kn<RB>(ks, 16 * kt, n, lane, f);
-                mma(s[n], a, f[0], f[1]);
-                mma(s[n + 1], a, f[2], f[3]);
-            }
-        }
-    }
-    if (p.dh0) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2*>(p.dh0 + prow * DK + 8 * n + 2 * tq) = f2(s[n][0], s[n][1]);
-            *reinterpret_cast<float2*>(p.dh0 + (prow + 8) * DK + 8 * n + 2 * tq) = f2(s[n][2], s[n][3]);
-        }
-    }
-}
 
 // ------------------------------------------------- everything else, by chunk ----
 template <int DK, int DV>
@@ -267,6 +66,23 @@ __device__ __forceinline__ void product(float (&acc)[NTC][4], uint32_t at, uint3
     }
 }
 
+// acc += A . B over the head's width: A [row][p], B [n][p], both in tiles of 64 p.
+template <int NTC, int DV, int DK>
+__device__ __forceinline__ void product_p(float (&acc)[NTC][4], uint32_t at, uint32_t bt, int m0, int nc0, int lane) {
+#pragma unroll
+    for (int kt = 0; kt < DV / 16; ++kt) {
+        uint32_t a[4];
+        load_a_mk<128>(at + (kt >> 2) * (C * 128), 16 * m0, 2 * (kt & 3), lane, a);
+#pragma unroll
+        for (int n = 0; n < NTC; n += 2) {
+            uint32_t f[4];
+            load_b_nk<128>(bt + (kt >> 2) * (DK * 128), 8 * (nc0 + n), 2 * (kt & 3), lane, f);
+            mma(acc[n], a, f[0], f[1]);
+            mma(acc[n + 1], a, f[2], f[3]);
+        }
+    }
+}
+
 template <int NTC>
 __device__ __forceinline__ void zero(float (&a)[NTC][4]) {
 #pragma unroll
@@ -292,7 +108,7 @@ __device__ __forceinline__ float2 row_dots(const float (&acc)[NTC][4], const uns
 template <int DK, int DV>
 __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
     using L = GradSmem<DK, DV>;
-    constexpr int RB = DK * 2, VB = DV * 2, NTC = DK / 16;
+    constexpr int RB = DK * 2, NTC = DK / 16;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int gq = lane >> 2, tq = lane & 3;
@@ -326,13 +142,15 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
         const int64_t rec = (b * p.nheads + h) * p.nchunks + ch;
         const int64_t voff = (b * p.seqlen + t0) * vstride + h * DV * 2;
         const unsigned char* rg = static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES;
-        load_tile<VB, C>(sm + L::DO, static_cast<const unsigned char*>(p.dout) + voff, vstride, valid, tid, 256);
-        load_tile<128, DV>(sm + L::U, static_cast<const unsigned char*>(p.u) + rec * DV * C * 2, C * 2, DV, tid, 256);
-        load_tile<128, DV>(sm + L::R, static_cast<const unsigned char*>(p.dr) + rec * DV * C * 2, C * 2, DV, tid, 256);
+#pragma unroll
+        for (int t = 0; t < DV / 64; ++t)
+            load_tile<128, C>(sm + L::DO + t * C * 128, static_cast<const unsigned char*>(p.dout) + voff + t * 128, vstride, valid, tid, 256);
+        load_image(sm + L::U, static_cast<const unsigned char*>(p.u) + rec * DV * C * 2, DV * C * 2, tid, 256);
+        load_image(sm + L::R, static_cast<const unsigned char*>(p.dr) + rec * DV * C * 2, DV * C * 2, tid, 256);
         if (tid < 48) cp_async_16(sm + L::F + tid * 16, rg + REC_F + tid * 16, 16);
         cp_async_commit();
-        load_tile<RB, DV>(sm + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * RB, RB, DV, tid, 256);
-        load_tile<RB, DV>(sm + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * RB, RB, DV, tid, 256);
+        load_image(sm + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * RB, DV * RB, tid, 256);
+        load_image(sm + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * RB, DV * RB, tid, 256);
         cp_async_commit();
         if (w == 7) {
             double s0, s1, last;
@@ -366,13 +184,13 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
 #pragma unroll
         for (int kt = 0; kt < DV / 16; ++kt) {
             uint32_t ao[4], ar[4];
-            load_a_mk<VB>(dos, 16 * mi, 2 * kt, lane, ao);
-            load_a_km<128>(rs, 16 * kt, 2 * mi, lane, ar);
+            load_a_mk<128>(dos + (kt >> 2) * (C * 128), 16 * mi, 2 * (kt & 3), lane, ao);
+            load_a_mk<128>(rs + (kt >> 2) * (C * 128), 16 * mi, 2 * (kt & 3), lane, ar);
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
                 if (4 * hf + n > 2 * mi + 1) break;
                 uint32_t f[4];
-                load_b_kn<128>(us, 16 * kt, 4 * hf + n, lane, f);
+                load_b_nk<128>(us + (kt >> 2) * (C * 128), 32 * hf + 8 * n, 2 * (kt & 3), lane, f);
                 mma(dp[n], ao, f[0], f[1]);
                 mma(dp[n + 1], ao, f[2], f[3]);
                 mma(da[n], ar, f[0], f[1]);
@@ -416,15 +234,15 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
             const int i = tid >> 2, part = tid & 3;
             float d = 0.0f;
             if (i < valid) {
-                const bf16* vg = static_cast<const bf16*>(p.v) + voff / 2 + i * (vstride / 2);
-#pragma unroll 4
-                for (int c = part * (DV / 4); c < (part + 1) * (DV / 4); c += 4) {
-                    const float4 vv = load4(vg + c);
-                    const unsigned char* rr = sm + L::R + (i & 7) * 2;
-                    d = fmaf(vv.x, load1(reinterpret_cast<const bf16*>(rr + tile_off<128>(c, i >> 3))), d);
-                    d = fmaf(vv.y, load1(reinterpret_cast<const bf16*>(rr + tile_off<128>(c + 1, i >> 3))), d);
-                    d = fmaf(vv.z, load1(reinterpret_cast<const bf16*>(rr + tile_off<128>(c + 2, i >> 3))), d);
-                    d = fmaf(vv.w, load1(reinterpret_cast<const bf16*>(rr + tile_off<128>(c + 3, i >> 3))), d);
+                const uint4* vg = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.v) + voff + i * vstride);
+#pragma unroll
+                for (int x = part * (DV / 32); x < (part + 1) * (DV / 32); ++x) {
+                    const uint4 vv = vg[x];
+                    const uint4 rr = *reinterpret_cast<const uint4*>(sm + L::R + (x >> 3) * (C * 128) + tile_off<128>(i, x & 7));
+                    d = fmaf(bf16_lo(vv.x), bf16_lo(rr.x), fmaf(bf16_hi(vv.x), bf16_hi(rr.x), d));
+                    d = fmaf(bf16_lo(vv.y), bf16_lo(rr.y), fmaf(bf16_hi(vv.y), bf16_hi(rr.y), d));
+                    d = fmaf(bf16_lo(vv.z), bf16_lo(rr.z), fmaf(bf16_hi(vv.z), bf16_hi(rr.z), d));
+                    d = fmaf(bf16_lo(vv.w), bf16_lo(rr.w), fmaf(bf16_hi(vv.w), bf16_hi(rr.w), d));
                 }
             }
             d += __shfl_xor_sync(0xffffffffu, d, 1);
@@ -441,7 +259,7 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
         float acc[NTC][4];
         {
             zero(acc);
-            product<NTC, DV / 16, false, VB, RB>(acc, dos, ss, mi, nc0, 0, 15, lane);
+            product_p<NTC, DV, DK>(acc, dos, ss, mi, nc0, lane);
             const float f0 = p.scale * eg[i0], f1 = p.scale * eg[i0 + 8];
             const float2 d = row_dots<NTC, RB>(acc, sm + L::Q, i0, nc0, tq);
             rc[0] = fmaf(f0, d.x, rc[0]);
@@ -456,7 +274,7 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
         }
         {
             zero(acc);
-            product<NTC, DV / 16, true, 128, RB>(acc, rs, ss, mi, nc0, 0, 15, lane);
+            product_p<NTC, DV, DK>(acc, rs, ss, mi, nc0, lane);
             const float f0 = eg[i0], f1 = eg[i0 + 8];
             const float2 d = row_dots<NTC, RB>(acc, sm + L::K, i0, nc0, tq);
             rb[0] = fmaf(-f0, d.x, rb[0]);
@@ -473,7 +291,7 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
         }
         {
             zero(acc);
-            product<NTC, DV / 16, true, 128, RB>(acc, us, dss, mi, nc0, 0, 15, lane);
+            product_p<NTC, DV, DK>(acc, us, dss, mi, nc0, lane);
             const float f0 = eg[C + i0], f1 = eg[C + i0 + 8];
             const float2 d = row_dots<NTC, RB>(acc, sm + L::K, i0, nc0, tq);
             rk[0] = f0 * d.x;
@@ -580,15 +398,6 @@ __global__ void __launch_bounds__(256, 1) gdr_bwd_grad_kernel(const GDRArgs p) {
     }
 }
 
-template <int DK, int NW>
-cudaError_t launch_bwd_chain(const GDRArgs& a, cudaStream_t s) {
-    constexpr int bytes = BwdChainSmem<DK, NW>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(gdr_bwd_chain_kernel<DK, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    gdr_bwd_chain_kernel<DK, NW><<<(unsigned)(a.batch * a.nheads * (a.headdim / (16 * NW))), 32 * NW, bytes, s>>>(a);
-    return cudaGetLastError();
-}
-
 template <int DK, int DV>
 cudaError_t launch_grad(const GDRArgs& a, cudaStream_t s) {
     constexpr int bytes = GradSmem<DK, DV>::BYTES;
@@ -601,8 +410,7 @@ cudaError_t launch_grad(const GDRArgs& a, cudaStream_t s) {
 
 template <int DK>
 cudaError_t launch_bwd(const GDRArgs& a, cudaStream_t s) {
-    const bool wide = a.headdim == 128 && a.batch * a.nheads * 2 > 148;
-    cudaError_t e = wide ? launch_bwd_chain<DK, 8>(a, s) : launch_bwd_chain<DK, 4>(a, s);
+    cudaError_t e = launch_gdr_chain(a, true, s);
     if (e != cudaSuccess) return e;
     return a.headdim == 64 ? launch_grad<DK, 64>(a, s) : launch_grad<DK, 128>(a, s);
 }

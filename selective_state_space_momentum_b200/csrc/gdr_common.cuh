@@ -16,6 +16,8 @@ constexpr int C = kGdrChunk;               // steps of a chunk
 //   Pm  (C, C) bf16   scale e^(c_i - c_j) q_i.k_j (j <= i)
 //   eg, tail, beta (C) fp32: e^(c_i), e^(c_last - c_i), beta_i
 // and, apart from it, Tlo (C, C) bf16, what T's rounding to bf16 left over.
+// The matrices are images of their shared-memory tiles (tile_off<128>), so
+// that they are copied piece by piece.
 constexpr int REC_T = 0, REC_P = C * C * 2, REC_F = 2 * C * C * 2;
 constexpr int REC_BYTES = REC_F + 3 * C * 4;
 static_assert(REC_BYTES == kGdrRecBytes, "record size");
@@ -30,18 +32,18 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c16) {
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ void stsm4t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
                  :: "r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -121,11 +123,23 @@ __device__ __forceinline__ void chunk_cumsum(const bf16* g, int64_t stride, int 
     last = __shfl_sync(0xffffffffu, run, 31);
 }
 
-// ROWS rows of RB bytes from global memory (row stride `stride` bytes) into a
-// tile, by all `nthreads` threads; rows from `valid` on become zeros.
-template <int RB, int ROWS>
+// The A operand back to a tile stored [k][m].
+template <int RB>
+__device__ __forceinline__ void store_a_km(uint32_t tile, int k0, int mc, int lane, const uint32_t (&r)[4]) {
+    const int m = lane >> 3;
+    stsm4t(tile + tile_off<RB>(k0 + (m >> 1) * 8 + (lane & 7), mc + (m & 1)), r[0], r[1], r[2], r[3]);
+}
+
+// `bytes` of a tile image from global memory to shared memory, piece by piece.
+__device__ __forceinline__ void load_image(unsigned char* dst, const void* src, int bytes, int tid, int nthreads) {
+    for (int i = tid * 16; i < bytes; i += nthreads * 16) cp_async_16(dst + i, static_cast<const unsigned char*>(src) + i, 16);
+}
+
+// ROWS rows of PIECES x 16 bytes from global memory (row stride `stride`
+// bytes) into a tile of RB-byte rows, by all `nthreads` threads; rows from
+// `valid` on become zeros.
+template <int RB, int ROWS, int PIECES = RB / 16>
 __device__ __forceinline__ void load_tile(unsigned char* tile, const void* src, int64_t stride, int valid, int tid, int nthreads) {
-    constexpr int PIECES = RB / 16;
     for (int i = tid; i < ROWS * PIECES; i += nthreads) {
         const int r = i / PIECES, c = i % PIECES;
         const bool in = r < valid;

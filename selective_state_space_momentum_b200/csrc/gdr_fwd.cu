@@ -10,88 +10,83 @@
 //     S'   = e^(c_last) S + sum_j e^(c_last - c_j) u_j k_j^T
 //
 // Two launches.  gdr_prep_kernel, parallel over chunks, forms T and the
-// masked q.k of every chunk (what does not depend on the state).
-// gdr_chain_kernel walks the chunks in order, one warp per 16 rows p of the
-// state: S^T lives in the warp's registers as fp32 accumulators, and since
-// the columns of the accumulators of one product are the A operand of the
-// next, S -> S k -> u -> S' needs no shared memory and no barrier between the
-// products; the rows p never meet.
+// masked q.k of every chunk (what does not depend on the state);
+// gdr_chain_kernel (gdr_chain.cu) walks the chunks in order.
 //
 // Precision: the state is fp32.  Where it enters a product it is split in two
 // bf16 terms (hi + lo, 2^-17), and so are v - e^c S k, T and e^c u; k, q, v are bf16
 // already.  The outputs o are rounded to bf16 anyway (2^-9), so the products
-// that reach only o take the hi terms alone.
+// that reach only o take the hi terms of u alone.
 #include "gdr_common.cuh"
 
 namespace mmscan {
 
 namespace gdr {
 
-constexpr int PITCH = 68;                  // floats of a row of A and T in shared memory
-
-template <int DK>
-constexpr int prep_smem() { return 2 * C * DK * 2 + 2 * C * PITCH * 4 + C * 8 + C * 4; }
-
-// c = a + b * (-1): rows [r0, r0 + n) etc. of T <- -(X . Y), used by the
-// block inverse below; each of `nt` threads forms EW neighbouring outputs.
-template <int DIM, int EW>
-__device__ __forceinline__ void block_product(float* out, const float* X, const float* Y, float sign, int t) {
-    const int r = t / (DIM / EW), c = (t % (DIM / EW)) * EW;
-    float acc[EW];
-#pragma unroll
-    for (int e = 0; e < EW; ++e) acc[e] = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < DIM; ++k) {
-        const float x = X[r * PITCH + k];
-#pragma unroll
-        for (int e = 0; e < EW; e += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(Y + k * PITCH + c + e);
-            acc[e] = fmaf(x, y.x, acc[e]);
-            acc[e + 1] = fmaf(x, y.y, acc[e + 1]);
-            acc[e + 2] = fmaf(x, y.z, acc[e + 2]);
-            acc[e + 3] = fmaf(x, y.w, acc[e + 3]);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < EW; e += 4)
-        *reinterpret_cast<float4*>(out + r * PITCH + c + e) =
-            make_float4(sign * acc[e], sign * acc[e + 1], sign * acc[e + 2], sign * acc[e + 3]);
-}
+// ---------------------------------------------- the chunks' own matrices ----
+// One CTA of four warps a chunk and head; warp w holds rows 16 w .. 16 w + 15.
+//
+// T = (I + A)^-1, in 16 x 16 blocks: T_ww by substitution in fp32, a lane a
+// column; below the diagonal T_ij = -T_ii sum_{j<=m<i} A_im T_mj, warp j its
+// block column j, on the tensor cores with every operand split in two bf16
+// terms.  This is forward substitution by blocks, so it is as stable as the
+// substitution is, whatever the size of A (a product of powers of A would not
+// be: their entries grow and cancel).
+//
+// Bound: latency of the dependent steps (loads, k.k, substitution, three
+// block rows), hidden by four to five CTAs an SM.
+struct PrepSmem {
+    // K and Q (2 C DK bf16 from 0 on) until the products are formed, then:
+    static constexpr int AH = 0, AL = 8192, PM = 16384, TH = 24576, TL = 32768;
+    static constexpr int DIAG = 40960, DP = 20;              // per warp: 16 x DP floats, column i of its diagonal block of A
+    static constexpr int CUM = DIAG + 4 * 16 * DP * 4;       // double c[C]
+    static constexpr int E = CUM + C * 8, F = E + C * 4, BETA = F + C * 4, WIDE = BETA + C * 4;
+    static constexpr int BYTES = WIDE + 16;
+};
 
 template <int DK>
 __global__ void __launch_bounds__(128) gdr_prep_kernel(const GDRArgs p) {
+    using L = PrepSmem;
     constexpr int RB = DK * 2;
     extern __shared__ __align__(1024) unsigned char sm[];
-    unsigned char* Kt = sm;
-    unsigned char* Qt = sm + C * RB;
-    float* A = reinterpret_cast<float*>(sm + 2 * C * RB);
-    float* T = A + C * PITCH;
-    double* cum = reinterpret_cast<double*>(T + C * PITCH);
-    float* beta = reinterpret_cast<float*>(cum + C);
+    double* cum = reinterpret_cast<double*>(sm + L::CUM);
+    float* ef = reinterpret_cast<float*>(sm + L::E);
+    float* ff = reinterpret_cast<float*>(sm + L::F);
+    float* beta = reinterpret_cast<float*>(sm + L::BETA);
+    int* wide = reinterpret_cast<int*>(sm + L::WIDE);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int64_t rec = blockIdx.x;                        // (b, h, chunk)
+    const int gq = lane >> 2, tq = lane & 3;
+    const int64_t rec = blockIdx.x;                          // (b, h, chunk)
     const int64_t bh = rec / p.nchunks, ch = rec - bh * p.nchunks;
     const int64_t b = bh / p.nheads, h = bh - b * p.nheads;
     const int64_t t0 = ch * C;
     const int valid = (int)(p.seqlen - t0 < C ? p.seqlen - t0 : C);
     const int64_t gk = ((b * p.seqlen + t0) * p.ngroups + h / (p.nheads / p.ngroups)) * DK;
     const int64_t kstride = p.ngroups * DK * 2;
-    load_tile<RB, C>(Kt, static_cast<const bf16*>(p.k) + gk, kstride, valid, tid, 128);
-    load_tile<RB, C>(Qt, static_cast<const bf16*>(p.q) + gk, kstride, valid, tid, 128);
+    load_tile<RB, C>(sm, static_cast<const bf16*>(p.k) + gk, kstride, valid, tid, 128);
+    load_tile<RB, C>(sm + C * RB, static_cast<const bf16*>(p.q) + gk, kstride, valid, tid, 128);
     cp_async_commit();
 
     unsigned char* out = static_cast<unsigned char*>(p.rec) + rec * REC_BYTES;
     float* fout = reinterpret_cast<float*>(out + REC_F);
     const int64_t gh = (b * p.seqlen + t0) * p.nheads + h;
     if (w == 0) {
-        const int r = 2 * lane;
         double s0, s1, last;
+        const int r = 2 * lane;
         chunk_cumsum(static_cast<const bf16*>(p.g) + gh, p.nheads, valid, lane, s0, s1, last);
         cum[r] = s0;
         cum[r + 1] = s1;
         *reinterpret_cast<float2*>(fout + r) = f2(ex2_approx((float)(s0 * kLog2e)), ex2_approx((float)(s1 * kLog2e)));
         *reinterpret_cast<float2*>(fout + C + r) =
             f2(ex2_approx((float)((last - s0) * kLog2e)), ex2_approx((float)((last - s1) * kLog2e)));
+        // e^(c_i - c_j) as the product of e^(c_i - mid) and e^(mid - c_j), where
+        // neither can leave fp32's range (2^60 either way); else by element
+        const double first = __shfl_sync(0xffffffffu, s0, 0), mid = 0.5 * (first + last);
+        const double a0 = (s0 - mid) * kLog2e, a1 = (s1 - mid) * kLog2e;
+        const bool far = __any_sync(0xffffffffu, !(fabs(a0) < 60.0) || !(fabs(a1) < 60.0));
+        *reinterpret_cast<float2*>(ef + r) = far ? f2(1.0f, 1.0f) : f2(ex2_approx((float)a0), ex2_approx((float)a1));
+        *reinterpret_cast<float2*>(ff + r) = far ? f2(1.0f, 1.0f) : f2(ex2_approx((float)-a0), ex2_approx((float)-a1));
+        if (lane == 0) *wide = far;
     } else if (w == 1) {
 #pragma unroll
         for (int r = lane; r < C; r += 32) {
@@ -103,335 +98,174 @@ __global__ void __launch_bounds__(128) gdr_prep_kernel(const GDRArgs p) {
     cp_async_wait<0>();
     __syncthreads();
 
-    // k.k and q.k: warp w the rows 16 w .. 16 w + 15, n-tiles up to the diagonal
+    // k.k and q.k, n-tiles up to the diagonal
     float kk[8][4], qk[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.0f;
-    const uint32_t ks = smem_u32(Kt), qs = smem_u32(Qt);
+    const uint32_t base = smem_u32(sm), qs = base + C * RB;
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt) {
         uint32_t ak[4], aq[4];
-        load_a_mk<RB>(ks, 16 * w, 2 * kt, lane, ak);
+        load_a_mk<RB>(base, 16 * w, 2 * kt, lane, ak);
         load_a_mk<RB>(qs, 16 * w, 2 * kt, lane, aq);
 #pragma unroll
         for (int n = 0; n < 8; n += 2) {
             if (n > 2 * w + 1) break;
             uint32_t bk[4];
-            load_b_nk<RB>(ks, 8 * n, 2 * kt, lane, bk);
+            load_b_nk<RB>(base, 8 * n, 2 * kt, lane, bk);
             mma(kk[n], ak, bk[0], bk[1]);
             mma(kk[n + 1], ak, bk[2], bk[3]);
             mma(qk[n], aq, bk[0], bk[1]);
             mma(qk[n + 1], aq, bk[2], bk[3]);
         }
     }
-    const int gq = lane >> 2, tq = lane & 3;
+    __syncthreads();                                         // K and Q give way to A, Pm and T
+    const int i0 = 16 * w + gq;
+    const float be[2] = {beta[i0], beta[i0 + 8]}, ei[2] = {ef[i0], ef[i0 + 8]};
+    if (*wide) {                                             // decays by element (the factors are ones then)
+        for (int n = 0; n <= 2 * w + 1; ++n)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int i = 16 * w + gq + 8 * half;
-        const double ci = cum[i];
-        const float bi = beta[i];
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + 8 * (e >> 1), jj = 8 * n + 2 * tq + (e & 1);
+                const float d = jj <= i ? ex2_approx((float)((cum[i] - cum[jj]) * kLog2e)) : 0.0f;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int j = 8 * n + 2 * tq;
-            float pv[2], av[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float d = j + e <= i ? ex2_approx((float)((ci - cum[j + e]) * kLog2e)) : 0.0f;
-                pv[e] = j + e <= i ? p.scale * qk[n][2 * half + e] * d : 0.0f;
-                av[e] = j + e < i ? bi * kk[n][2 * half + e] * d : 0.0f;
+                for (int m = 0; m < 8; ++m)
+                    if (m == n) {
+                        kk[m][e] *= d;
+                        qk[m][e] *= d;
+                    }
             }
-            *reinterpret_cast<float2*>(A + i * PITCH + j) = f2(av[0], av[1]);
-            *reinterpret_cast<uint32_t*>(out + REC_P + (i * C + j) * 2) = pack_bf16x2(pv[0], pv[1]);
-        }
     }
-    __syncthreads();
-
-    // T = (I + A)^-1 in fp32: the diagonal 16 x 16 blocks by substitution, a
-    // lane a column, then twice the join [[Ta, 0], [-Tb A_ba Ta, Tb]].  Every
-    // step is a forward substitution over blocks, as stable as the
-    // substitution itself.  The upper blocks of T hold the joins' inner products.
-    if (lane < 16) {
-        const float* Ab = A + 16 * w * PITCH + 16 * w;
+    float* diag = reinterpret_cast<float*>(sm + L::DIAG) + w * 16 * L::DP;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        uint32_t pm[2] = {0u, 0u};
+        if (n <= 2 * w + 1) {
+            const int j = 8 * n + 2 * tq;
+            const float2 fj = *reinterpret_cast<const float2*>(ff + j);
+            float av[4], pv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + 8 * (e >> 1), jj = j + (e & 1);
+                const float d = ei[e >> 1] * ((e & 1) ? fj.y : fj.x);
+                pv[e] = jj <= i ? p.scale * qk[n][e] * d : 0.0f;
+                av[e] = jj < i ? be[e >> 1] * kk[n][e] * d : 0.0f;
+            }
+            pm[0] = pack_bf16x2(pv[0], pv[1]);
+            pm[1] = pack_bf16x2(pv[2], pv[3]);
+            if (n >= 2 * w) {                                // the diagonal block, by columns
+#pragma unroll
+                for (int e = 0; e < 4; ++e) diag[(j + (e & 1) - 16 * w) * L::DP + gq + 8 * (e >> 1)] = av[e];
+            } else {
+                uint32_t hi[2], lo[2];
+                split2(av[0], av[1], hi[0], lo[0]);
+                split2(av[2], av[3], hi[1], lo[1]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t off = tile_off<128>(i0 + 8 * r, n) + 4 * tq;
+                    *reinterpret_cast<uint32_t*>(sm + L::AH + off) = hi[r];
+                    *reinterpret_cast<uint32_t*>(sm + L::AL + off) = lo[r];
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) *reinterpret_cast<uint32_t*>(sm + L::PM + tile_off<128>(i0 + 8 * r, n) + 4 * tq) = pm[r];
+    }
+    __syncwarp();
+    if (lane < 16) {                                         // T_ww, column `lane`
         float t[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == lane ? 1.0f : 0.0f;
+        for (int i = 0; i < 16; ++i) t[i] = i == lane ? 1.0f : 0.0f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) s = fmaf(-Ab[i * PITCH + m], t[m], s);
-            t[i] = s;
-            T[(16 * w + i) * PITCH + 16 * w + lane] = s;
+        for (int i = 0; i < 15; ++i) {
+            float a[16];
+#pragma unroll
+            for (int q = (i + 1) / 4; q < 4; ++q) *reinterpret_cast<float4*>(a + 4 * q) = *reinterpret_cast<const float4*>(diag + i * L::DP + 4 * q);
+#pragma unroll
+            for (int r = i + 1; r < 16; ++r) t[r] = fmaf(-a[r], t[i], t[r]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const bf16 hi = __float2bfloat16_rn(t[i]);
+            const uint32_t off = tile_off<128>(16 * w + i, 2 * w + (lane >> 3)) + 2 * (lane & 7);
+            *reinterpret_cast<bf16*>(sm + L::TH + off) = hi;
+            *reinterpret_cast<bf16*>(sm + L::TL + off) = __float2bfloat16_rn(t[i] - __bfloat162float(hi));
         }
     }
     __syncthreads();
-    {
-        const int a = 32 * (tid >> 6), t = tid & 63;       // blocks (a, a) and (a + 16, a + 16)
-        block_product<16, 4>(T + a * PITCH + a + 16, A + (a + 16) * PITCH + a, T + a * PITCH + a, 1.0f, t);
-        __syncthreads();
-        block_product<16, 4>(T + (a + 16) * PITCH + a, T + (a + 16) * PITCH + a + 16, T + a * PITCH + a + 16, -1.0f, t);
-        __syncthreads();
-        // the scratch blocks inside the 32 x 32 diagonal blocks back to zero
-        *reinterpret_cast<float4*>(T + (a + t / 4) * PITCH + a + 16 + 4 * (t & 3)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        __syncthreads();
-        block_product<32, 8>(T + 32, A + 32 * PITCH, T, 1.0f, tid);
-        __syncthreads();
-        block_product<32, 8>(T + 32 * PITCH, T + 32 * PITCH + 32, T + 32, -1.0f, tid);
-        __syncthreads();
+    // block column w: X = T_iw^T (16 columns w x 16 rows i) as the A operand
+    if (w < 3) {
+        uint32_t xh[3][4], xl[3][4];
+        load_a_km<128>(base + L::TH, 16 * w, 2 * w, lane, xh[0]);
+        load_a_km<128>(base + L::TL, 16 * w, 2 * w, lane, xl[0]);
+#pragma unroll
+        for (int d = 1; d < 4; ++d) {
+            const int i = w + d;
+            if (i > 3) break;
+            float acc[2][4], tr[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[0][e] = acc[1][e] = tr[0][e] = tr[1][e] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < d; ++m) {
+                uint32_t fh[4], fl[4];
+                load_b_nk<128>(base + L::AH, 16 * i, 2 * (w + m), lane, fh);
+                load_b_nk<128>(base + L::AL, 16 * i, 2 * (w + m), lane, fl);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    mma(acc[t], xh[m], fh[2 * t], fh[2 * t + 1]);
+                    mma(acc[t], xl[m], fh[2 * t], fh[2 * t + 1]);
+                    mma(acc[t], xh[m], fl[2 * t], fl[2 * t + 1]);
+                }
+            }
+            uint32_t sh[4], sl[4], fh[4], fl[4];
+            acc_to_a2<2>(acc, 0, sh, sl);
+            load_b_nk<128>(base + L::TH, 16 * i, 2 * i, lane, fh);
+            load_b_nk<128>(base + L::TL, 16 * i, 2 * i, lane, fl);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                mma(tr[t], sh, fh[2 * t], fh[2 * t + 1]);
+                mma(tr[t], sl, fh[2 * t], fh[2 * t + 1]);
+                mma(tr[t], sh, fl[2 * t], fl[2 * t + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tr[t][e] = -tr[t][e];
+            }
+            acc_to_a2<2>(tr, 0, sh, sl);
+            store_a_km<128>(base + L::TH, 16 * i, 2 * w, lane, sh);
+            store_a_km<128>(base + L::TL, 16 * i, 2 * w, lane, sl);
+            if (d < 3)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    xh[d][e] = sh[e];
+                    xl[d][e] = sl[e];
+                }
+        }
     }
-    // T in two bf16 terms
+    __syncthreads();
     unsigned char* lo_out = static_cast<unsigned char*>(p.tlo) + rec * (C * C * 2);
-    const int r = tid >> 1, c0 = 32 * (tid & 1);
 #pragma unroll
-    for (int c = c0; c < c0 + 32; c += 8) {
+    for (int i = tid; i < C * C * 2 / 16; i += 128) {
+        const int r = i >> 3, c = (i & 7) ^ (r & 7);         // row and 8-column piece of the image's piece i
         uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-        if (r >= 32 || c < 32) {                             // the block above the diagonal is scratch
-            const float* s = T + r * PITCH + c;
-            split2(s[0], s[1], hi.x, lo.x);
-            split2(s[2], s[3], hi.y, lo.y);
-            split2(s[4], s[5], hi.z, lo.z);
-            split2(s[6], s[7], hi.w, lo.w);
+        if (c / 2 <= r / 16) {                               // T is zero above the diagonal blocks
+            hi = *reinterpret_cast<const uint4*>(sm + L::TH + i * 16);
+            lo = *reinterpret_cast<const uint4*>(sm + L::TL + i * 16);
         }
-        *reinterpret_cast<uint4*>(out + REC_T + (r * C + c) * 2) = hi;
-        *reinterpret_cast<uint4*>(lo_out + (r * C + c) * 2) = lo;
+        *reinterpret_cast<uint4*>(out + REC_T + i * 16) = hi;
+        *reinterpret_cast<uint4*>(out + REC_P + i * 16) = *reinterpret_cast<const uint4*>(sm + L::PM + i * 16);
+        *reinterpret_cast<uint4*>(lo_out + i * 16) = lo;
     }
-}
-
-// ------------------------------------------------------------- the chain ----
-template <int DK, int NW>
-struct ChainSmem {
-    static constexpr int K = 0, Q = C * DK * 2, T = 2 * C * DK * 2, TL = T + C * C * 2, PM = TL + C * C * 2;
-    static constexpr int V = PM + C * C * 2, VB = 32 * NW;            // bytes of a row of V
-    static constexpr int F = V + C * (VB < 128 ? 128 : VB), STAGE = F + 1024;
-    static constexpr int BYTES = 2 * STAGE + 1024;
-    static_assert(VB == 128 || VB == 256, "a row of V is a tile row");
-};
-
-template <int DK, int NW, bool TRAIN>
-__global__ void __launch_bounds__(32 * NW, 1) gdr_chain_kernel(const GDRArgs p) {
-    using L = ChainSmem<DK, NW>;
-    constexpr int RB = DK * 2, VB = L::VB, NT = DK / 8, DVT = 16 * NW, NTH = 32 * NW;
-    extern __shared__ __align__(1024) unsigned char sm[];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int gq = lane >> 2, tq = lane & 3;
-    const int tiles = p.headdim / DVT;
-    const int64_t bh = blockIdx.x / tiles;
-    const int p0 = (int)(blockIdx.x % tiles) * DVT;
-    const int64_t b = bh / p.nheads, h = bh - b * p.nheads;
-    const int64_t kstride = p.ngroups * DK * 2, vstride = p.nheads * p.headdim * 2;
-    const unsigned char* kg = static_cast<const unsigned char*>(p.k) + b * p.seqlen * kstride + h / (p.nheads / p.ngroups) * DK * 2;
-    const unsigned char* qg = static_cast<const unsigned char*>(p.q) + b * p.seqlen * kstride + h / (p.nheads / p.ngroups) * DK * 2;
-    const unsigned char* vg = static_cast<const unsigned char*>(p.v) + b * p.seqlen * vstride + (h * p.headdim + p0) * 2;
-
-    auto issue = [&](int64_t ch) {
-        unsigned char* st = sm + (ch & 1) * L::STAGE;
-        const int64_t t0 = ch * C;
-        const int valid = (int)(p.seqlen - t0 < C ? p.seqlen - t0 : C);
-        const int64_t rec = bh * p.nchunks + ch;
-        const unsigned char* rg = static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES;
-        load_tile<RB, C>(st + L::K, kg + t0 * kstride, kstride, valid, tid, NTH);
-        load_tile<RB, C>(st + L::Q, qg + t0 * kstride, kstride, valid, tid, NTH);
-        load_tile<128, C>(st + L::T, rg + REC_T, 128, C, tid, NTH);
-        load_tile<128, C>(st + L::TL, static_cast<const unsigned char*>(p.tlo) + rec * (C * C * 2), 128, C, tid, NTH);
-        load_tile<128, C>(st + L::PM, rg + REC_P, 128, C, tid, NTH);
-        load_tile<VB, C>(st + L::V, vg + t0 * vstride, vstride, valid, tid, NTH);
-        if (tid < 48) cp_async_16(st + L::F + tid * 16, rg + REC_F + tid * 16, 16);
-        cp_async_commit();
-    };
-
-    // S^T of this warp's rows p: accumulator tile n holds states 8 n .. 8 n + 7
-    const int64_t prow = bh * p.headdim + p0 + 16 * w + gq;
-    float s[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float2 x = f2(0.0f, 0.0f), y = x;
-        if (p.h0) {
-            x = *reinterpret_cast<const float2*>(p.h0 + prow * DK + 8 * n + 2 * tq);
-            y = *reinterpret_cast<const float2*>(p.h0 + (prow + 8) * DK + 8 * n + 2 * tq);
-        }
-        s[n][0] = x.x; s[n][1] = x.y; s[n][2] = y.x; s[n][3] = y.y;
-    }
-    issue(0);
-    for (int64_t ch = 0; ch < p.nchunks; ++ch) {
-        cp_async_wait<0>();
-        __syncthreads();                     // this chunk is there, and every warp is done with the other slot
-        if (ch + 1 < p.nchunks) issue(ch + 1);
-        unsigned char* st = sm + (ch & 1) * L::STAGE;
-        const uint32_t ks = smem_u32(st + L::K), qs = smem_u32(st + L::Q), ts = smem_u32(st + L::T),
-                       tl = smem_u32(st + L::TL), ps = smem_u32(st + L::PM), vs = smem_u32(st + L::V);
-        const float* eg = reinterpret_cast<const float*>(st + L::F);
-        const int64_t rec = bh * p.nchunks + ch;
-
-        if constexpr (TRAIN) {               // the state at the chunk's start, for the backward (bf16)
-            bf16* sv = static_cast<bf16*>(p.states) + (rec * p.headdim + p0 + 16 * w + gq) * DK + 2 * tq;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                *reinterpret_cast<uint32_t*>(sv + 8 * n) = pack_bf16x2(s[n][0], s[n][1]);
-                *reinterpret_cast<uint32_t*>(sv + 8 * DK + 8 * n) = pack_bf16x2(s[n][2], s[n][3]);
-            }
-        }
-        // x = S k (16 rows p x 64 steps), o = S q
-        float x[8][4], o[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[n][e] = o[n][e] = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt) {
-            uint32_t hi[4], lo[4];
-            acc_to_a2<NT>(s, kt, hi, lo);
-#pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-                uint32_t f[4];
-                load_b_nk<RB>(ks, 8 * n, 2 * kt, lane, f);
-                mma(x[n], hi, f[0], f[1]);
-                mma(x[n + 1], hi, f[2], f[3]);
-                mma(x[n], lo, f[0], f[1]);
-                mma(x[n + 1], lo, f[2], f[3]);
-                load_b_nk<RB>(qs, 8 * n, 2 * kt, lane, f);
-                mma(o[n], hi, f[0], f[1]);
-                mma(o[n + 1], hi, f[2], f[3]);
-            }
-        }
-        // x <- beta (v - e^c x), o <- scale e^c o
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-            uint32_t vv[4];
-            const int m = lane >> 3;
-            ldsm4t(vs + tile_off<VB>(8 * n + (m >> 1) * 8 + (lane & 7), 2 * w + (m & 1)), vv);
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const int j = 8 * (n + d) + 2 * tq;
-                const float2 e = *reinterpret_cast<const float2*>(eg + j);
-                const float2 be = *reinterpret_cast<const float2*>(eg + 2 * C + j);
-                float(&xx)[4] = x[n + d];
-                xx[0] = be.x * fmaf(-e.x, xx[0], bf16_lo(vv[2 * d]));
-                xx[1] = be.y * fmaf(-e.y, xx[1], bf16_hi(vv[2 * d]));
-                xx[2] = be.x * fmaf(-e.x, xx[2], bf16_lo(vv[2 * d + 1]));
-                xx[3] = be.y * fmaf(-e.y, xx[3], bf16_hi(vv[2 * d + 1]));
-                float(&oo)[4] = o[n + d];
-                oo[0] *= p.scale * e.x; oo[1] *= p.scale * e.y; oo[2] *= p.scale * e.x; oo[3] *= p.scale * e.y;
-            }
-        }
-        // u = x T^T (T lower triangular: step j reaches rows i >= j)
-        float u[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[n][e] = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t hi[4], lo[4];
-            acc_to_a2<8>(x, kt, hi, lo);
-#pragma unroll
-            for (int n = 2 * kt; n < 8; n += 2) {
-                uint32_t f[4];
-                load_b_nk<128>(ts, 8 * n, 2 * kt, lane, f);
-                mma(u[n], hi, f[0], f[1]);
-                mma(u[n + 1], hi, f[2], f[3]);
-                mma(u[n], lo, f[0], f[1]);
-                mma(u[n + 1], lo, f[2], f[3]);
-                load_b_nk<128>(tl, 8 * n, 2 * kt, lane, f);
-                mma(u[n], hi, f[0], f[1]);
-                mma(u[n + 1], hi, f[2], f[3]);
-            }
-        }
-        if constexpr (TRAIN) {               // u for the backward, (P, C) bf16
-            bf16* uv = static_cast<bf16*>(p.u) + (rec * p.headdim + p0 + 16 * w + gq) * C + 2 * tq;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                *reinterpret_cast<uint32_t*>(uv + 8 * n) = pack_bf16x2(u[n][0], u[n][1]);
-                *reinterpret_cast<uint32_t*>(uv + 8 * C + 8 * n) = pack_bf16x2(u[n][2], u[n][3]);
-            }
-        }
-        // o += u Pm^T
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t a[4];
-            acc_to_a<8>(u, kt, a);
-#pragma unroll
-            for (int n = 2 * kt; n < 8; n += 2) {
-                uint32_t f[4];
-                load_b_nk<128>(ps, 8 * n, 2 * kt, lane, f);
-                mma(o[n], a, f[0], f[1]);
-                mma(o[n + 1], a, f[2], f[3]);
-            }
-        }
-        // S <- e^(c_last) S + (tail u) k
-        const float last = eg[C - 1];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] *= last;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float2 tl2 = *reinterpret_cast<const float2*>(eg + C + 8 * n + 2 * tq);
-            u[n][0] *= tl2.x; u[n][1] *= tl2.y; u[n][2] *= tl2.x; u[n][3] *= tl2.y;
-        }
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t hi[4], lo[4];
-            acc_to_a2<8>(u, kt, hi, lo);
-#pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t f[4];
-                load_b_kn<RB>(ks, 16 * kt, n, lane, f);
-                mma(s[n], hi, f[0], f[1]);
-                mma(s[n + 1], hi, f[2], f[3]);
-                mma(s[n], lo, f[0], f[1]);
-                mma(s[n + 1], lo, f[2], f[3]);
-            }
-        }
-        // o through the warp's own columns of V's tile (read above) to memory
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-            const int m = lane >> 3;
-            stsm4t(vs + tile_off<VB>(8 * n + (m >> 1) * 8 + (lane & 7), 2 * w + (m & 1)), pack_bf16x2(o[n][0], o[n][1]),
-                   pack_bf16x2(o[n][2], o[n][3]), pack_bf16x2(o[n + 1][0], o[n + 1][1]), pack_bf16x2(o[n + 1][2], o[n + 1][3]));
-        }
-        __syncwarp();
-        const int valid = (int)(p.seqlen - ch * C < C ? p.seqlen - ch * C : C);
-        unsigned char* og = static_cast<unsigned char*>(p.o) + (b * p.seqlen + ch * C) * vstride + (h * p.headdim + p0 + 16 * w) * 2;
-#pragma unroll
-        for (int i = lane; i < 2 * C; i += 32) {
-            const int r = i >> 1, c = i & 1;
-            if (r < valid)
-                *reinterpret_cast<uint4*>(og + r * vstride + c * 16) =
-                    *reinterpret_cast<const uint4*>(st + L::V + tile_off<VB>(r, 2 * w + c));
-        }
-    }
-    if (p.hT) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2*>(p.hT + prow * DK + 8 * n + 2 * tq) = f2(s[n][0], s[n][1]);
-            *reinterpret_cast<float2*>(p.hT + (prow + 8) * DK + 8 * n + 2 * tq) = f2(s[n][2], s[n][3]);
-        }
-    }
-}
-
-template <int DK, int NW, bool TRAIN>
-cudaError_t launch_chain(const GDRArgs& a, cudaStream_t s) {
-    constexpr int bytes = ChainSmem<DK, NW>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(gdr_chain_kernel<DK, NW, TRAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    const int64_t blocks = a.batch * a.nheads * (a.headdim / (16 * NW));
-    gdr_chain_kernel<DK, NW, TRAIN><<<(unsigned)blocks, 32 * NW, bytes, s>>>(a);
-    return cudaGetLastError();
 }
 
 template <int DK>
 cudaError_t launch_fwd(const GDRArgs& a, cudaStream_t s) {
-    constexpr int bytes = prep_smem<DK>();
+    constexpr int bytes = PrepSmem::BYTES;
     cudaError_t e = cudaFuncSetAttribute(gdr_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     gdr_prep_kernel<DK><<<(unsigned)(a.batch * a.nheads * a.nchunks), 128, bytes, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // A warp's products fill a quarter of its scheduler's tensor pipe time
-    // alone; two warps a scheduler (NW = 8) pay once the GPU is full.
-    const bool wide = a.headdim == 128 && a.batch * a.nheads * 2 > 148;
-    if (a.states) return wide ? launch_chain<DK, 8, true>(a, s) : launch_chain<DK, 4, true>(a, s);
-    return wide ? launch_chain<DK, 8, false>(a, s) : launch_chain<DK, 4, false>(a, s);
+    return launch_gdr_chain(a, false, s);
 }
 
 }  // namespace gdr

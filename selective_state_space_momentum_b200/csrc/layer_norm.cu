@@ -12,15 +12,19 @@
 // an element).  A row is kept in the registers of TPR threads, so that the
 // mean, the centred sum of squares (two passes over registers: no
 // cancellation when the mean is large) and the output take one read of
-// memory.  All statistics and sums are fp32.  TPR is the smallest of 8, 32,
-// 128, 512, 1024 whose threads hold the row in 16 elements each: short rows
-// (a head's 64 channels) share a warp, so each thread still moves 16 bytes
-// at a time and the reductions stay in shuffles.
+// memory.  All statistics and sums are fp32.
 //
-// The weight's gradient: a block walks rows in a grid-stride loop with the
-// sums of its columns in registers, writes one partial row to the workspace,
+// The forward gives each group of TPR threads one row (16 elements a thread)
+// and lets many small blocks overlap.  The backward keeps 8 elements a thread
+// and as many blocks as the SMs hold; they walk the rows in a grid-stride loop
+// with the next row's loads issued before this row's sums, the weights and
+// the sums of a thread's columns in registers over all its rows.
+//
+// The weight's gradient: every block writes one partial row to the workspace,
 // and a second kernel adds the partials in block order: no atomics, so the
 // result is bit-identical from run to run.
+#include <type_traits>
+
 #include "mm_common.cuh"
 #include "mm_internal.h"
 
@@ -28,7 +32,6 @@ namespace mmscan {
 
 namespace {
 
-constexpr int kElems = 16;        // elements of a row a thread holds, at most
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.0f, 1.0f + ex2_approx(-z * kLog2e)); }
 
@@ -104,6 +107,14 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* red, int& slot) {
 
 constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
 
+// VEC elements as they are in memory (the next row's, while this one's are used).
+template <typename IO, int VEC>
+struct Raw {
+    typename std::conditional<VEC == 1, IO, uint4>::type v;
+    __device__ __forceinline__ void load(const IO* p) { v = *reinterpret_cast<const decltype(v)*>(p); }
+    __device__ __forceinline__ void get(float* f) const { load_vec<IO, VEC>(reinterpret_cast<const IO*>(&v), f); }
+};
+
 template <typename IO, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArgs p) {
     constexpr int RPB = norm_block(TPR) / TPR;
@@ -166,10 +177,13 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArg
     }
 }
 
-// Backward.  Rows go to blocks in a grid-stride loop; dw, db of this thread's
-// columns stay in registers over all its rows.
-template <typename IO, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(const NormArgs p) {
+// Resident blocks an SM that the backward's grid counts on: 24 warps at 8
+// elements a thread (up to 80 registers), 16 at 16 (128 registers; a block of
+// 1024 threads has 64 and spills).
+constexpr int norm_bwd_resident(int bt, int elems) { return bt >= 512 ? 1 : elems > 8 ? 512 / bt : 768 / bt; }
+
+template <typename IO, int VEC, int TPR, int NV, bool GATE>
+__global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(TPR), NV * VEC)) norm_bwd_kernel(const NormArgs p) {
     constexpr int BT = norm_block(TPR);
     constexpr int RPB = BT / TPR;
     __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
@@ -177,16 +191,38 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(const NormArg
     const int t = threadIdx.x % TPR;
     const int grp = threadIdx.x / TPR;
     const int cols = (int)p.cols;
-    float dw[NV * VEC], db[NV * VEC];
+    float dw[NV * VEC], db[NV * VEC], w[NV * VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * TPR) * VEC;
+        load_param<VEC>(p.weight && c < cols ? p.weight + c : nullptr, w + i * VEC, 1.0f);
+    }
 #pragma unroll
     for (int i = 0; i < NV * VEC; ++i) dw[i] = db[i] = 0.0f;
 
-    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += (int64_t)gridDim.x * RPB) {
-        const bool active = r0 + grp < p.rows;
-        const int64_t row = active ? r0 + grp : p.rows - 1;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    Raw<IO, VEC> rx[NV], ry[NV], rz[GATE ? NV : 1];
+    float mean, rstd;
+    auto fetch = [&](int64_t r0) {
+        const int64_t row = r0 + grp < p.rows ? r0 + grp : p.rows - 1;     // idle groups follow along (shuffles)
+        mean = p.rms ? 0.0f : p.mean[row];
+        rstd = p.rstd[row];
         const int64_t base = row * cols;
-        const float mean = p.rms ? 0.0f : p.mean[row];
-        const float rstd = p.rstd[row];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * TPR) * VEC;
+            if (c >= cols) continue;
+            rx[i].load(static_cast<const IO*>(p.x) + base + c);
+            ry[i].load(static_cast<const IO*>(p.dy) + base + c);
+            if constexpr (GATE) rz[i].load(static_cast<const IO*>(p.z) + base + c);
+        }
+    };
+    int64_t r0 = (int64_t)blockIdx.x * RPB;
+    fetch(r0);
+    for (; r0 < p.rows; r0 += step) {
+        const bool active = r0 + grp < p.rows;
+        const int64_t base = (r0 + grp) * cols;
+        const float rs = rstd;
         float xh[NV * VEC], d[NV * VEC];
         float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -195,22 +231,21 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(const NormArg
 #pragma unroll
             for (int e = 0; e < VEC; ++e) xh[i * VEC + e] = d[i * VEC + e] = 0.0f;
             if (c >= cols) continue;
-            load_vec<IO, VEC>(static_cast<const IO*>(p.x) + base + c, xh + i * VEC);
-            load_vec<IO, VEC>(static_cast<const IO*>(p.dy) + base + c, d + i * VEC);
-            float w[VEC];
-            load_param<VEC>(p.weight ? p.weight + c : nullptr, w, 1.0f);
+            rx[i].get(xh + i * VEC);
+            ry[i].get(d + i * VEC);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) xh[i * VEC + e] = (xh[i * VEC + e] - mean) * rstd;
-            if (p.z) {
+            for (int e = 0; e < VEC; ++e) xh[i * VEC + e] = (xh[i * VEC + e] - mean) * rs;
+            if constexpr (GATE) {
                 float z[VEC], b[VEC], dz[VEC];
-                load_vec<IO, VEC>(static_cast<const IO*>(p.z) + base + c, z);
+                rz[i].get(z);
                 load_param<VEC>(p.bias ? p.bias + c : nullptr, b, 0.0f);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
+                    const int k = i * VEC + e;
                     const float sg = sigmoid_f32(z[e]);
-                    const float n = fmaf(xh[i * VEC + e], w[e], b[e]);
-                    dz[e] = d[i * VEC + e] * n * sg * fmaf(z[e], 1.0f - sg, 1.0f);
-                    d[i * VEC + e] *= z[e] * sg;
+                    const float n = fmaf(xh[k], w[k], b[e]);
+                    dz[e] = d[k] * n * sg * fmaf(z[e], 1.0f - sg, 1.0f);
+                    d[k] *= z[e] * sg;
                 }
                 if (active && p.dz) store_vec<IO, VEC>(static_cast<IO*>(p.dz) + base + c, dz);
             }
@@ -221,11 +256,12 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(const NormArg
                     dw[k] = fmaf(d[k], xh[k], dw[k]);
                     db[k] += d[k];
                 }
-                d[k] *= w[e];
+                d[k] *= w[k];
                 s.x += d[k];
                 s.y = fmaf(d[k], xh[k], s.y);
             }
         }
+        if (r0 + step < p.rows) fetch(r0 + step);
         s = row_sum<TPR>(s, red, slot);
         const float a0 = p.rms ? 0.0f : s.x * p.inv_cols;
         const float a1 = s.y * p.inv_cols;
@@ -239,7 +275,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(const NormArg
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int k = i * VEC + e;
-                    o[e] = rstd * (d[k] - a0 - xh[k] * a1);
+                    o[e] = rs * (d[k] - a0 - xh[k] * a1);
                 }
                 store_vec<IO, VEC>(dx + c, o);
             }
@@ -299,6 +335,7 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float* part, int
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
     if (c < 2 * cols)
+#pragma unroll 4
         for (int b = threadIdx.y; b < nblk; b += 32) s += part[(int64_t)b * 2 * cols + c];
     acc[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -315,78 +352,76 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float* part, int
 }
 
 template <typename IO, int VEC, int TPR, int NV>
-cudaError_t launch_one(const NormArgs& a, bool bwd, cudaStream_t s) {
-    constexpr int BT = norm_block(TPR);
-    constexpr int RPB = BT / TPR;
-    if (!bwd) {
-        const int64_t blocks = (a.rows + RPB - 1) / RPB;
-        if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        norm_fwd_kernel<IO, VEC, TPR, NV><<<(unsigned)blocks, BT, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    norm_bwd_kernel<IO, VEC, TPR, NV><<<(unsigned)norm_bwd_blocks(a.rows, a.cols), BT, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.part) return e;
-    norm_param_kernel<<<(unsigned)((2 * a.cols + 31) / 32), dim3(32, 32), 0, s>>>(
-        a.part, norm_bwd_blocks(a.rows, a.cols), a.cols, a.dweight, a.dbias);
+cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
+    constexpr int BT = norm_block(TPR), RPB = BT / TPR;
+    const int64_t blocks = (a.rows + RPB - 1) / RPB;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    norm_fwd_kernel<IO, VEC, TPR, NV><<<(unsigned)blocks, BT, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-// Threads of one row: the smallest count whose threads hold it in kElems
-// elements each.
-int norm_tpr(int64_t cols) {
-    return cols <= 8 * kElems ? 8 : cols <= 32 * kElems ? 32 : cols <= 128 * kElems ? 128 : cols <= 512 * kElems ? 512 : 1024;
+template <typename IO, int VEC, int TPR, int NV>
+cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s) {
+    const int blocks = norm_bwd_blocks(a.rows, a.cols);
+    if (a.z) norm_bwd_kernel<IO, VEC, TPR, NV, true><<<blocks, norm_block(TPR), 0, s>>>(a);
+    else norm_bwd_kernel<IO, VEC, TPR, NV, false><<<blocks, norm_block(TPR), 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.part) return e;
+    norm_param_kernel<<<(unsigned)((2 * a.cols + 31) / 32), dim3(32, 32), 0, s>>>(a.part, blocks, a.cols, a.dweight, a.dbias);
+    return cudaGetLastError();
 }
 
-template <typename IO, int VEC, int TPR>
-cudaError_t launch_tpr(const NormArgs& a, bool bwd, cudaStream_t s) {
-    const int64_t nv = (a.cols + (int64_t)TPR * VEC - 1) / (TPR * VEC);
-    if constexpr (VEC == 1) {
-        if (nv <= 4) return launch_one<IO, VEC, TPR, 4>(a, bwd, s);
-        if (nv <= 8) return launch_one<IO, VEC, TPR, 8>(a, bwd, s);
-        return launch_one<IO, VEC, TPR, 16>(a, bwd, s);
-    } else {
-        if (nv <= 1) return launch_one<IO, VEC, TPR, 1>(a, bwd, s);
-        if (VEC == 8 || nv <= 2) return launch_one<IO, VEC, TPR, 2>(a, bwd, s);
-        return launch_one<IO, VEC, TPR, 16 / VEC>(a, bwd, s);
-    }
+// Forward: threads of a row at 16 elements each (8 in rows of up to 256).
+// Measured (33.5 M elements in rows of 2048, bf16): 61 us at 16 elements, 81 at
+// 8, 65 at 64 (a warp a row); 84 for a grid that stays and walks the rows.
+template <typename IO, int VEC>
+cudaError_t launch_fwd_vec(const NormArgs& a, cudaStream_t s) {
+    if (a.cols <= 64) return launch_fwd<IO, VEC, 8, 8 / VEC>(a, s);
+    if (a.cols <= 256) return launch_fwd<IO, VEC, 32, 8 / VEC>(a, s);
+    if (a.cols <= 512) return launch_fwd<IO, VEC, 32, 16 / VEC>(a, s);
+    if (a.cols <= 2048) return launch_fwd<IO, VEC, 128, 16 / VEC>(a, s);
+    if (a.cols <= 4096) return launch_fwd<IO, VEC, 256, 16 / VEC>(a, s);
+    if (a.cols <= 8192) return launch_fwd<IO, VEC, 512, 16 / VEC>(a, s);
+    return launch_fwd<IO, VEC, 1024, 16 / VEC>(a, s);
+}
+
+// Backward: threads of a row at 8 elements each, 16 past 2048 columns.
+int norm_bwd_tpr(int64_t cols) {
+    return cols <= 64 ? 8 : cols <= 256 ? 32 : cols <= 1024 ? 128 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
 }
 
 template <typename IO, int VEC>
-cudaError_t launch_vec(const NormArgs& a, bool bwd, cudaStream_t s) {
-    switch (norm_tpr(a.cols)) {
-        case 8: return launch_tpr<IO, VEC, 8>(a, bwd, s);
-        case 32: return launch_tpr<IO, VEC, 32>(a, bwd, s);
-        case 128: return launch_tpr<IO, VEC, 128>(a, bwd, s);
-        case 512: return launch_tpr<IO, VEC, 512>(a, bwd, s);
-        default: return launch_tpr<IO, VEC, 1024>(a, bwd, s);
+cudaError_t launch_bwd_vec(const NormArgs& a, cudaStream_t s) {
+    switch (norm_bwd_tpr(a.cols)) {
+        case 8: return launch_bwd<IO, VEC, 8, 8 / VEC>(a, s);
+        case 32: return launch_bwd<IO, VEC, 32, 8 / VEC>(a, s);
+        case 128: return launch_bwd<IO, VEC, 128, 8 / VEC>(a, s);
+        case 256: return a.cols <= 2048 ? launch_bwd<IO, VEC, 256, 8 / VEC>(a, s) : launch_bwd<IO, VEC, 256, 16 / VEC>(a, s);
+        case 512: return launch_bwd<IO, VEC, 512, 16 / VEC>(a, s);
+        default: return launch_bwd<IO, VEC, 1024, 16 / VEC>(a, s);
     }
-}
-
-template <typename IO>
-cudaError_t launch_io(const NormArgs& a, bool bwd, cudaStream_t s) {
-    // Rows of whole 16-byte pieces move 16 bytes at a time, others by element.
-    constexpr int VEC = 16 / sizeof(IO);
-    return a.cols % VEC == 0 ? launch_vec<IO, VEC>(a, bwd, s) : launch_vec<IO, 1>(a, bwd, s);
 }
 
 }  // namespace
 
-// Blocks of the backward: enough to fill 148 SMs at the register use of its
-// threads (about 1024 of them an SM), and no more than there are rows.
+// Blocks of the backward: what 148 SMs hold at once, and no more than there
+// are rows.
 int norm_bwd_blocks(int64_t rows, int64_t cols) {
-    const int tpr = norm_tpr(cols), bt = norm_block(tpr);
+    const int tpr = norm_bwd_tpr(cols), bt = norm_block(tpr);
     const int64_t need = (rows + bt / tpr - 1) / (bt / tpr);
-    const int64_t fill = 148 * (1024 / bt);
+    const int64_t fill = 148 * norm_bwd_resident(bt, cols <= 2048 ? 8 : 16);
     return (int)(need < fill ? need : fill);
 }
 
+// Rows of whole 16-byte pieces move 16 bytes at a time, others by element.
 cudaError_t launch_norm_fwd(const NormArgs& a, int io, cudaStream_t s) {
-    return io == 0 ? launch_io<float>(a, false, s) : launch_io<bf16>(a, false, s);
+    if (io == 0) return a.cols % 4 == 0 ? launch_fwd_vec<float, 4>(a, s) : launch_fwd_vec<float, 1>(a, s);
+    return a.cols % 8 == 0 ? launch_fwd_vec<bf16, 8>(a, s) : launch_fwd_vec<bf16, 1>(a, s);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, int io, cudaStream_t s) {
-    return io == 0 ? launch_io<float>(a, true, s) : launch_io<bf16>(a, true, s);
+    if (io == 0) return a.cols % 4 == 0 ? launch_bwd_vec<float, 4>(a, s) : launch_bwd_vec<float, 1>(a, s);
+    return a.cols % 8 == 0 ? launch_bwd_vec<bf16, 8>(a, s) : launch_bwd_vec<bf16, 1>(a, s);
 }
 
 }  // namespace mmscan

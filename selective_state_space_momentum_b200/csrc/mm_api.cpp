@@ -71,23 +71,13 @@ int64_t seg_len_for(int64_t batch, int64_t L, int64_t dim, int64_t dstate, int i
 
 using mmscan::aligned16;
 using mmscan::inject_launch_failure;
+using mmscan::inject_stall;
 using mmscan::kMaxIndex;
 using mmscan::kMaxSeqlen;
 using mmscan::mul_ok;
 using mmscan::overlap;
 using mmscan::Range;
 using mmscan::rng;
-
-// Test hook for the device-side give-up path: with MMSCAN_FAULT_INJECT=stall
-// the kernels that stage their inputs through bounded waits (the two forward
-// scans, the backward, the SSD kernel) are launched with their producer told
-// to issue nothing.  Nothing is then in flight; every wait runs out after its
-// limit, the kernel returns, and mm_device_status reports
-// MM_ERR_DEVICE_TIMEOUT.  The outputs of such a call are undefined.
-int inject_stall() {
-    const char* v = std::getenv("MMSCAN_FAULT_INJECT");
-    return (v && std::strcmp(v, "stall") == 0) ? 1 : 0;
-}
 
 // Test hook for the sequence-split path's fallback: with
 // MMSCAN_FAULT_INJECT=records its request for record memory asks for more
@@ -201,6 +191,22 @@ mm_status report(mm_status st, const char* fmt, ...) {
 
 mm_status report_ok() { return ok(); }
 
+namespace {
+constexpr int kMaxReaders = 8;
+unsigned int (*g_readers[kMaxReaders])() = {};
+int g_num_readers = 0;
+}  // namespace
+
+void register_error_reader(unsigned int (*read_and_clear)()) {
+    if (g_num_readers < kMaxReaders) g_readers[g_num_readers++] = read_and_clear;
+}
+
+unsigned int read_registered_errors() {
+    unsigned int w = 0;
+    for (int i = 0; i < g_num_readers; ++i) w |= g_readers[i]();
+    return w;
+}
+
 }  // namespace mmscan
 
 extern "C" {
@@ -228,7 +234,8 @@ int mm_version(void) { return 100; }
 mm_status mm_device_status(void) {
     const cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return from_cuda(e, "mm_device_status: synchronize");
-    const unsigned int w = mmscan::scan_read_and_clear_device_error() |
+    const unsigned int w = mmscan::read_registered_errors() |
+                           mmscan::scan_read_and_clear_device_error() |
                            mmscan::scan_seg_read_and_clear_device_error() |
                            mmscan::scan_bwd_read_and_clear_device_error() |
                            mmscan::ssd_read_and_clear_device_error() |

@@ -46,4 +46,15 @@ inline bool inject_launch_failure() {
     return v && std::strcmp(v, "launch") == 0;
 }
 
+// Test hook for the device-side give-up path: with MMSCAN_FAULT_INJECT=stall
+// the kernels that stage their inputs through bounded waits (the two forward
+// scans, the backward, the SSD kernels, the gated delta rule) are launched with their producer told
+// to issue nothing.  Nothing is then in flight; every wait runs out after its
+// limit, the kernel returns, and mm_device_status reports
+// MM_ERR_DEVICE_TIMEOUT.  The outputs of such a call are undefined.
+inline int inject_stall() {
+    const char* v = std::getenv("MMSCAN_FAULT_INJECT");
+    return (v && std::strcmp(v, "stall") == 0) ? 1 : 0;
+}
+
 }  // namespace mmscan

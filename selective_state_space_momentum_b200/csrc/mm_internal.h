@@ -15,6 +15,10 @@ namespace mmscan {
 mm_status report(mm_status st, const char* fmt, ...);
 mm_status report_ok();
 
+// Add a kernel file's reader of its device error word to mm_device_status
+// (called while the library is loaded, before any entry point).
+void register_error_reader(unsigned int (*read_and_clear)());
+
 // Release the side streams and events the host-buffer entry points keep for
 // the calling thread (created again on the next call that needs them).
 void host_pipeline_release();
@@ -207,6 +211,7 @@ cudaError_t launch_ssd_fwd(const SSDArgs& a, cudaStream_t s);
 
 // Gated delta rule (gdr_fwd.cu, gdr_bwd.cu): chunks of kGdrChunk steps.
 constexpr int kGdrChunk = 64;
+constexpr int kGdrTile = 64;               // state rows (of headdim) of one chain
 constexpr int kGdrRecBytes = 2 * kGdrChunk * kGdrChunk * 2 + 3 * kGdrChunk * 4;   // a chunk's record
 
 // Arguments of one gated-delta-rule call over a sequence (device pointers;
@@ -221,7 +226,8 @@ struct GDRArgs {
     void* o;               // (batch, L, H, P)
     float* hT;             // (batch, H, P, N) or null
     // per (batch row, head, chunk): the record, the low part of T, and for the
-    // backward the state at the chunk's start (P, N) and the rows written (P, C)
+    // backward, by tiles of kGdrTile rows p, the state at the chunk's start
+    // (N, tile) and the rows written (C, tile), bf16
     void* rec;
     void* tlo;
     void* states;          // null: no backward will follow
@@ -238,8 +244,9 @@ struct GDRArgs {
     void* dg;              // (batch, L, H)
     void* dbeta;
     float* dh0;            // (batch, H, P, N) or null
-    void* dstates;         // per chunk: the gradient reaching the state at its end (P, N) bf16
-    void* dr;              // per chunk: T^T du (P, C) bf16
+    void* dstates;         // laid out like states: the gradient reaching the state at a chunk's end
+    void* dr;              // laid out like u: T^T du
+    int stall;             // test only: stage no input, so that the bounded waits run out
 };
 
 // Arguments of one decode step of the gated delta rule.
@@ -260,6 +267,8 @@ bool gdr_shape_supported(int64_t headdim, int64_t dstate);
 cudaError_t launch_gdr_fwd(const GDRArgs& a, cudaStream_t s);
 cudaError_t launch_gdr_bwd(const GDRArgs& a, cudaStream_t s);
 cudaError_t launch_gdr_step(const GDRStepArgs& a, int io, cudaStream_t s);
+// The chain over the chunks (gdr_chain.cu), forward or backward.
+cudaError_t launch_gdr_chain(const GDRArgs& a, bool backward, cudaStream_t s);
 
 // Arguments of one layer norm call, forward or backward.
 struct NormArgs {
