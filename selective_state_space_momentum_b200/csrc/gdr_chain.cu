@@ -16,17 +16,27 @@
 //     2. T^T x                                         r; dv = beta r; -beta e^c r
 //     3. dS += [k; q]^T [-beta e^c r; scale e^c do]    next chunk: dS to bf16, dS <- e^c_last dS
 // Products 1, 2, 3 of a chunk and the epilogues between them are one chain of
-// dependences; 0 and 4 run beside it.
+// dependences; 0 and 4 run beside it (4 during the next chunk's first epilogue).
+// Two terms of an operand B are two 64-column groups of one product with
+// N = 128, whose halves the epilogue adds: a step of 16 costs some 60 cycles
+// with 64 columns and 85 with 128.
 //
-// Roles (10 warps): warps 0-7 the epilogues (a thread one TMEM lane and 32 of
+// Roles (11 warps): warps 0-7 the epilogues (a thread one TMEM lane and 32 of
 // the 64 columns; lanes 0-63, the rows of k, carry the chain, lanes 64-127,
-// those of q, finish o), warp 8 the TMA loads (no multicast) into a ring of two
-// slots, warp 9 every tcgen05.mma.  Every wait is an mbarrier wait bounded by
-// kWaitLimitNs; on give-up the kernel records the fact, every role leaves its
-// loop, TMEM is freed and the kernel returns.
+// those of q, finish o), then one warp for the TMA loads (no multicast) into a
+// ring of two slots, one for every tcgen05.mma, and one for the stores, as bulk
+// copies of tiles: a thread's own columns of a row would be 32 lines to a store
+// instruction, and the queue behind it is the one the chain's shared-memory
+// accesses wait in.  Every wait is an mbarrier wait bounded by kWaitLimitNs; on
+// give-up the kernel records the fact, every role leaves its loop, waits for
+// its own copies, TMEM is freed and the kernel returns.
 //
-// Bound: the latency of the chain -- three products of at most 0.4 us and three
-// passes TMEM -> registers -> shared memory a chunk -- not tensor rate or bytes.
+// Bound: the latency of the chain -- three products and three passes TMEM ->
+// registers -> shared memory a chunk -- not tensor rate or bytes.  Measured, a
+// chunk of 64 steps (128 states, 64 rows, 128 CTAs): 2.4 us forward, 2.1 us
+// backward.  What mattered: one arrival a warp (3.2 us with one a thread),
+// waits that sleep in hardware (2.8 us polling), products issued by a warp
+// that runs together, its number known to be uniform (2.6 us from one lane).
 #include <cuda.h>
 
 #include "gdr_common.cuh"
@@ -41,9 +51,11 @@ namespace {
 
 constexpr int PT = kGdrTile;               // state rows p of a CTA
 constexpr int SLAB = 128 * 128;            // 64 columns of the stacked [k; q] tile
-constexpr int NEPI = 256, NTHREADS = NEPI + 64, W_PROD = 8, W_MMA = 9;
-constexpr uint32_t TM_S = 0, TM_X = 64, TM_U = 128, TM_O = 192, TM_COLS = 256;
-enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_P1 = 5, B_X = 6, B_P2 = 7, B_V = 8, B_P3 = 9, B_P4 = 10, B_OFREE = 11, B_DO = 12, NBAR = 13 };
+constexpr int CW = 32;                     // columns a thread
+constexpr int EPI_WARPS = 4 * PT / CW, NTHREADS = 32 * EPI_WARPS + 96, W_PROD = EPI_WARPS, W_MMA = W_PROD + 1, W_STORE = W_PROD + 2;
+constexpr int NPAIR = CW / 2;
+constexpr uint32_t TM_S = 0, TM_X = 128, TM_U = 256, TM_O = 384, TM_COLS = 512;   // S, X, U: two halves of 64, forward
+enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_P1 = 5, B_X = 6, B_P2 = 7, B_V = 8, B_P3 = 9, B_P4 = 10, B_OFREE = 11, B_DO = 12, B_OUT = 13, B_STORED = 14, NBAR = 15 };
 
 // Shared memory: a ring of two slots (the stacked k and q, [T; Pm], T's low
 // part, v or do, the decays), then the operand tiles the epilogues write.
@@ -52,14 +64,12 @@ struct Smem {
     static constexpr int KQ = 0, TP = DK / 64 * SLAB, TL = TP + 16384, V = TL + 8192, F = V + 8192, SLOT = F + 1024;
     static constexpr int SH = 2 * SLOT, SL = SH + DK * 128;      // S: [n][64 p] bf16, hi and lo
     static constexpr int XH = SL + DK * 128, XL = XH + 8192;     // x, then tail u: [step][64 p], hi and lo
-    static constexpr int U = XL + 8192;                          // u: [step][64 p]
-    static constexpr int BAR = U + 8192, TSLOT = BAR + NBAR * 8, ABORT = TSLOT + 8;
+    static constexpr int U = XL + 8192;                          // u (backward: r): [step][64 p]
+    static constexpr int OUT = U + 8192;                         // o (backward: dv): [step][64 p]
+    static constexpr int BAR = OUT + 8192, TSLOT = BAR + NBAR * 8, ABORT = TSLOT + 8;
     static constexpr int BYTES = ABORT + 8 + 1024;
     static_assert(BYTES <= 227 * 1024 && SLOT % 1024 == 0 && SH % 1024 == 0 && XH % 1024 == 0, "shared memory");
 };
-
-constexpr uint32_t ID_KM_MN = umma_idesc_bf16(128, 64, 0, 1);    // A K-major, B MN-major
-constexpr uint32_t ID_MN_MN = umma_idesc_bf16(128, 64, 1, 1);
 
 // `bytes` (a multiple of 16) of consecutive global memory into shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -67,41 +77,137 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// 32 fp32 values to 4 (hi) or 8 (hi and lo) pieces of 16 bytes of row `row`.
-__device__ __forceinline__ void put_row(unsigned char* tile, int row, int half, const uint32_t (&w)[16]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(tile + tile_off<128>(row, 4 * half + c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+// `bytes` of shared memory to consecutive global memory (this thread's bulk group).
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" :: "l"(dst), "r"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void split_row(const uint32_t (&r)[32], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) split2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), hi[e], lo[e]);
-}
-__device__ __forceinline__ void round_row(const uint32_t (&r)[32], uint32_t (&hi)[16]) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) hi[e] = pack_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    uint32_t a[16], b[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        a[e] = r[e];
-        b[e] = r[16 + e];
+
+// mbar_wait for waits on the critical path: a try may sleep in hardware for up
+// to 20 us (a polling warp takes issue slots and shared-memory cycles from the
+// ones that work), and the limit's clock is read only between tries.
+__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, unsigned int* err) {
+    unsigned long long t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
+        if (ok) return true;
+        const unsigned long long now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            atomicOr(err, kDevErrTimeout);
+            return false;
+        }
     }
-    tmem_st16(taddr, a);
-    tmem_st16(taddr + 16, b);
+}
+
+// One product step and the commit, by the elected lane (always the same) of a
+// warp that runs together: the operands stay in uniform registers (23 cycles a
+// step to issue, against 52 from a single lane's branch).
+__device__ __forceinline__ void umma_elect(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+                 :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+                 :: "r"(bar) : "memory");
+}
+
+// 16 consecutive 32-bit TMEM columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)), "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+// This thread's CW columns from `taddr` on; the sum of the two halves of a
+// product (64 columns apart).
+__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&a)[16]) { tmem_ld16(taddr, a); }
+__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&a)[32]) { tmem_ld32(taddr, a); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&a)[CW]) {
+#pragma unroll
+    for (int k = 0; k < CW; k += 16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = a[k + e];
+        tmem_st16(taddr + k, w);
+    }
+}
+__device__ __forceinline__ void tmem_get(uint32_t taddr, float2 (&x)[NPAIR]) {
+    uint32_t a[CW];
+    tmem_issue(taddr, a);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < NPAIR; ++e) x[e] = f2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+}
+__device__ __forceinline__ void tmem_get_sum(uint32_t taddr, float2 (&x)[NPAIR]) {
+    uint32_t a[CW], b[CW];
+    tmem_issue(taddr, a);
+    tmem_issue(taddr + 64, b);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < NPAIR; ++e)
+        x[e] = add2(f2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), f2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])));
+}
+// CW values to pieces of 16 bytes of row `row` of a tile.
+__device__ __forceinline__ void put_row(unsigned char* tile, int row, int part, const uint32_t (&w)[NPAIR]) {
+#pragma unroll
+    for (int c = 0; c < CW / 8; ++c)
+        *reinterpret_cast<uint4*>(tile + tile_off<128>(row, CW / 8 * part + c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
+__device__ __forceinline__ void split_row(const float2 (&x)[NPAIR], uint32_t (&hi)[NPAIR], uint32_t (&lo)[NPAIR]) {
+#pragma unroll
+    for (int e = 0; e < NPAIR; ++e) {
+        hi[e] = pack_bf16x2(x[e].x, x[e].y);
+        const float2 d = add2(x[e], f2(-bf16_lo(hi[e]), -bf16_hi(hi[e])));
+        lo[e] = pack_bf16x2(d.x, d.y);
+    }
+}
+__device__ __forceinline__ void round_row(const float2 (&x)[NPAIR], float scale, uint32_t (&hi)[NPAIR]) {
+#pragma unroll
+    for (int e = 0; e < NPAIR; ++e) {
+        const float2 y = mul2(f2(scale, scale), x[e]);
+        hi[e] = pack_bf16x2(y.x, y.y);
+    }
+}
+__device__ __forceinline__ void round_row(const float2 (&x)[NPAIR], uint32_t (&hi)[NPAIR]) {
+#pragma unroll
+    for (int e = 0; e < NPAIR; ++e) hi[e] = pack_bf16x2(x[e].x, x[e].y);
 }
 
 template <int DK, bool BWD>
 __global__ void __launch_bounds__(NTHREADS, 1)
 gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                 const __grid_constant__ CUtensorMap tm_v, const GDRArgs p) {
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const GDRArgs p) {
     using L = Smem<DK>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     unsigned char* smem = smem_raw + (base - raw_addr);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int tiles = p.headdim / PT;
     const int64_t bh = blockIdx.x / tiles;
     const int pt = (int)(blockIdx.x % tiles);
@@ -114,17 +220,19 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
             mbar_init(bar(B_FULL + k), 1);
-            mbar_init(bar(B_EMPTY + k), NEPI + 1);
+            mbar_init(bar(B_EMPTY + k), EPI_WARPS + 1);
         }
-        mbar_init(bar(B_S), NEPI);
+        mbar_init(bar(B_S), EPI_WARPS);
         mbar_init(bar(B_P1), 1);
-        mbar_init(bar(B_X), NEPI / 2);
+        mbar_init(bar(B_X), EPI_WARPS / 2);
         mbar_init(bar(B_P2), 1);
-        mbar_init(bar(B_V), NEPI / 2);
+        mbar_init(bar(B_V), EPI_WARPS / 2);
         mbar_init(bar(B_P3), 1);
         mbar_init(bar(B_P4), 1);
-        mbar_init(bar(B_OFREE), NEPI / 2);
-        mbar_init(bar(B_DO), NEPI / 2);
+        mbar_init(bar(B_OFREE), EPI_WARPS / 2);
+        mbar_init(bar(B_DO), EPI_WARPS / 2);
+        mbar_init(bar(B_OUT), EPI_WARPS / 2);
+        mbar_init(bar(B_STORED), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -135,7 +243,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::TSLOT);
     auto wait = [&](int i, int phase) -> bool {
         if (*abort_flag) return false;
-        if (!mbar_wait(bar(i), (uint32_t)phase & 1u, &g_gdr_dev_err)) {
+        if (!mbar_wait_sleep(bar(i), (uint32_t)phase & 1u, &g_gdr_dev_err)) {
             *abort_flag = 1;
             return false;
         }
@@ -165,20 +273,24 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
         }
     } else if (warp == W_MMA) {
-        if (lane == 0) {
+        {
+            auto mwait = [&](int bi, int phase) { return __all_sync(0xffffffffu, wait(bi, phase)); };
             // D (+)= A . B over ks steps of 16: A from `a` (K-major: 32 bytes a step
-            // within a slab of 64; MN-major: 16 rows a step), B from `bt` (MN-major)
-            auto prod_km = [&](uint32_t d, uint32_t a, uint32_t bt, int ks, bool acc) {
+            // within a slab of 64; MN-major: 16 rows a step), B from `bt` (MN-major,
+            // 64-column groups `ldb` apart), N = 64 or 128
+            auto prod_km = [&](uint32_t d, uint32_t a, uint32_t bt, uint32_t ldb, int N, int ks, bool acc) {
+                const uint32_t id = umma_idesc_bf16(128, N, 0, 1);
+                const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(bt, ldb, 1024);
 #pragma unroll
                 for (int s = 0; s < ks; ++s)
-                    umma_ss(tmem + d, umma_desc_sw128(a + (s >> 2) * SLAB + (s & 3) * 32, 16, 1024),
-                            umma_desc_sw128(bt + s * 2048, 8192, 1024), ID_KM_MN, acc || s > 0);
+                    umma_elect(tmem + d, da + (((s >> 2) * SLAB + (s & 3) * 32) >> 4), db + ((s * 2048) >> 4), id, acc || s > 0);
             };
-            auto prod_mn = [&](uint32_t d, uint32_t a, uint32_t lbo, uint32_t bt, int ks, bool acc) {
+            auto prod_mn = [&](uint32_t d, uint32_t a, uint32_t lbo, uint32_t bt, int N, int ks, bool acc) {
+                const uint32_t id = umma_idesc_bf16(128, N, 1, 1);
+                const uint64_t da = umma_desc_sw128(a, lbo, 1024), db = umma_desc_sw128(bt, 8192, 1024);
 #pragma unroll
                 for (int s = 0; s < ks; ++s)
-                    umma_ss(tmem + d, umma_desc_sw128(a + s * 2048, lbo, 1024), umma_desc_sw128(bt + s * 2048, 8192, 1024),
-                            ID_MN_MN, acc || s > 0);
+                    umma_elect(tmem + d, da + ((s * 2048) >> 4), db + ((s * 2048) >> 4), id, acc || s > 0);
             };
             // the second 64 rows of an M of 128 that has only 64: any tile will do,
             // its results go to lanes nobody reads
@@ -187,240 +299,275 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int c = 0; c < n && live; ++c) {
                 const uint32_t slot = base + (c & 1) * L::SLOT;
                 const uint32_t kq = slot + L::KQ, tp = slot + L::TP, tl = slot + L::TL;
-                if (!(live = wait(B_FULL + (c & 1), c >> 1))) break;
+                if (!(live = mwait(B_FULL + (c & 1), c >> 1))) break;
                 if constexpr (BWD) {                       // Pm^T do, beside the chain
                     tc_fence_after();
-                    prod_mn(TM_O, tp + 8192, 8192, slot + L::V, C / 16, false);
+                    prod_mn(TM_O, tp + 8192, 8192, slot + L::V, 64, C / 16, false);
                 }
-                if (!(live = wait(B_S, c))) break;
+                if (!(live = mwait(B_S, c))) break;
                 tc_fence_after();
-                prod_km(TM_X, kq, base + L::SH, DK / 16, false);
-                if constexpr (!BWD) prod_km(TM_X, kq, base + L::SL, DK / 16, true);
-                umma_commit(bar(B_P1));
-                if (!(live = wait(B_X, c))) break;
+                prod_km(TM_X, kq, base + L::SH, DK * 128, BWD ? 64 : 128, DK / 16, false);
+                commit_elect(bar(B_P1));
+                if (!(live = mwait(B_X, c))) break;
                 tc_fence_after();
                 if constexpr (BWD) {
-                    prod_mn(TM_U, tp, 8192, base + L::XH, C / 16, false);
+                    prod_mn(TM_U, tp, 8192, base + L::XH, 64, C / 16, false);
                 } else {
-                    prod_km(TM_U, tp, base + L::XH, C / 16, false);
-                    prod_km(TM_U, tl, base + L::XH, C / 16, true);
-                    prod_km(TM_U, tp, base + L::XL, C / 16, true);
+                    prod_km(TM_U, tp, base + L::XH, 8192, 128, C / 16, false);
+                    prod_km(TM_U, tl, base + L::XH, 8192, 64, C / 16, true);
                 }
-                umma_commit(bar(B_P2));
-                if (!(live = wait(B_V, c))) break;
+                commit_elect(bar(B_P2));
+                if (!(live = mwait(B_V, c))) break;
                 if constexpr (BWD) {
-                    if (!(live = wait(B_DO, c))) break;
+                    if (!(live = mwait(B_DO, c))) break;
                 }
                 tc_fence_after();
-                if constexpr (BWD) {
-                    prod_mn(TM_S, kq, lbo_k, base + L::XH, 2 * C / 16, true);     // [k; q]^T . [-beta e^c r; scale e^c do]
-                    umma_commit(bar(B_P3));
-                } else {
-                    prod_mn(TM_S, kq, lbo_k, base + L::XH, C / 16, true);
-                    prod_mn(TM_S, kq, lbo_k, base + L::XL, C / 16, true);
-                    umma_commit(bar(B_P3));
-                    if (!(live = wait(B_OFREE, c + 1))) break;
+                // backward: [k; q]^T . [-beta e^c r; scale e^c do]
+                prod_mn(TM_S, kq, lbo_k, base + L::XH, BWD ? 64 : 128, BWD ? 2 * C / 16 : C / 16, true);
+                commit_elect(bar(B_P3));
+                if constexpr (!BWD) {                      // [T; Pm] u, beside the next chunk's first epilogue
+                    if (!(live = mwait(B_OFREE, c + 1))) break;
                     tc_fence_after();
-                    prod_km(TM_O, tp, base + L::U, C / 16, false);
-                    umma_commit(bar(B_P4));
+                    prod_km(TM_O, tp, base + L::U, 8192, 64, C / 16, false);
+                    commit_elect(bar(B_P4));
                 }
-                umma_commit(bar(B_EMPTY + (c & 1)));
+                commit_elect(bar(B_EMPTY + (c & 1)));
             }
             // the last commit must land before the CTA may exit
-            if (live && !*abort_flag) wait(B_EMPTY + ((n - 1) & 1), (n - 1) >> 1);
+            if (live) mwait(B_EMPTY + ((n - 1) & 1), (n - 1) >> 1);
+        }
+    } else if (warp == W_STORE) {
+        // Per chunk: the state's tile, then o of the chunk before and u (backward:
+        // r and dv).  B_STORED: the tiles may be written again.
+        if (lane == 0) {
+            unsigned char* states = static_cast<unsigned char*>(BWD ? p.dstates : p.states);
+            unsigned char* rows = static_cast<unsigned char*>(BWD ? p.dr : p.u);
+            const int64_t first = bh * p.nchunks;
+            auto store_out = [&](int c) {
+                tma_store_4d(&tm_o, base + L::OUT, pt * PT, (int)h, (int)(chunk_of(c) * C), (int)b);
+            };
+            bool live = true;
+            for (int c = 0; c < n; ++c) {
+                const int64_t tile = (first + chunk_of(c)) * tiles + pt;
+                if (states) {
+                    if (!(live = wait(B_S, c))) break;
+                    bulk_store(states + tile * (DK * PT * 2), base + L::SH, DK * PT * 2);
+                }
+                if constexpr (BWD) {
+                    if (!(live = wait(B_OUT, c))) break;
+                    store_out(c);
+                    bulk_store(rows + tile * (C * PT * 2), base + L::U, C * PT * 2);
+                } else {
+                    if (c > 0) {
+                        if (!(live = wait(B_OUT, c - 1))) break;
+                        store_out(c - 1);
+                    }
+                    if (rows) {
+                        if (!(live = wait(B_V, c))) break;
+                        bulk_store(rows + tile * (C * PT * 2), base + L::U, C * PT * 2);
+                    }
+                }
+                bulk_commit_group();
+                bulk_wait_read_all();
+                mbar_arrive(bar(B_STORED));
+            }
+            if constexpr (!BWD) {
+                if (live && wait(B_OUT, n - 1)) {
+                    store_out(n - 1);
+                    bulk_commit_group();
+                }
+            }
+            bulk_wait_all();                               // complete before the CTA exits
         }
     } else {
-        const int q = warp & 3, half = warp >> 2;
+        const int q = warp & 3, part = warp >> 2;          // TMEM lanes 32 q .., columns CW part ..
         const int t = 32 * q + lane;                       // TMEM lane: state n, or row of [k; q]
         const bool krows = q < 2;                          // lanes 0-63
         const int i = t & 63;                              // step of the chunk
-        const uint32_t lb = tmem + ((uint32_t)(q * 32) << 16) + 32 * half;
+        const uint32_t lb = tmem + ((uint32_t)(q * 32) << 16) + CW * part;
         const bool states = t < DK;                        // (whole warps)
         auto wwait = [&](int bi, int phase) { return __all_sync(0xffffffffu, wait(bi, phase)); };
+        // One arrival a warp: arrivals on one mbarrier are taken one by one.
+        auto arrive = [&](int bi) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bi));
+        };
         // (batch, H, P, N): state n = t, rows p of this thread
-        const int64_t sbase = (bh * p.headdim + pt * PT + 32 * half) * DK + t;
+        const int64_t sbase = (bh * p.headdim + pt * PT + CW * part) * DK + t;
         const float* s0 = BWD ? p.dhT : p.h0;
-        uint32_t r[32];
+        float2 x[NPAIR];
+        uint32_t hi[NPAIR], lo[NPAIR], y[CW];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = s0 && states ? __float_as_uint(s0[sbase + (int64_t)e * DK]) : 0u;
-        tmem_st32(lb + TM_S, r);
+        for (int e = 0; e < CW; ++e) y[e] = s0 && states ? __float_as_uint(s0[sbase + (int64_t)e * DK]) : 0u;
+        tmem_store(lb + TM_S, y);
+        uint32_t zeros[CW];
+#pragma unroll
+        for (int e = 0; e < CW; ++e) zeros[e] = 0u;
+        if constexpr (!BWD) tmem_store(lb + TM_S + 64, zeros);
         tmem_wait_st();
 
-        float qs[32];                                      // lanes 64-127, forward: scale e^c S q of the chunk before
-        auto put_o = [&](int64_t ch) {                     // o = qs + Pm u, row i of chunk ch
-            tmem_ld32(lb + TM_O, r);
-            tmem_wait_ld();
+        float2 qs[NPAIR];                                      // lanes 64-127, forward: scale e^c S q of the chunk before
+        auto put_o = [&] {                                 // o = qs + Pm u, row i
+            tmem_get(lb + TM_O, x);
             tc_fence_before();
-            mbar_arrive(bar(B_OFREE));
-            if (ch * C + i >= p.seqlen) return;
-            uint32_t w[16];
+            arrive(B_OFREE);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                w[e] = pack_bf16x2(qs[2 * e] + __uint_as_float(r[2 * e]), qs[2 * e + 1] + __uint_as_float(r[2 * e + 1]));
-            uint4* o = reinterpret_cast<uint4*>(static_cast<bf16*>(p.o) + ((b * p.seqlen + ch * C + i) * p.nheads + h) * p.headdim + pt * PT + 32 * half);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < NPAIR; ++e) x[e] = add2(x[e], qs[e]);
+            round_row(x, hi);
+            put_row(smem + L::OUT, i, part, hi);
+            fence_proxy_async_smem();
+            arrive(B_OUT);
         };
 
         bool ok = true;
         for (int c = 0; c < n; ++c) {
             const unsigned char* slot = smem + (c & 1) * L::SLOT;
             const float* f = reinterpret_cast<const float*>(slot + L::F);
-            const int64_t ch = chunk_of(c), rec = bh * p.nchunks + ch;
-            uint32_t hi[16], lo[16];
             if (!(ok = wwait(B_FULL + (c & 1), c >> 1))) break;
-            if (c > 0 && !(ok = wwait(B_P3, c - 1))) break;
-            // S as operand tiles; S <- e^(c_last) S in place
+            const float last = f[C - 1], eg = f[i], tail = f[C + i], beta = f[2 * C + i];
+            if (c > 0 && !(ok = wwait(B_STORED, c - 1) && wwait(B_P3, c - 1))) break;
+            // S <- e^(c_last) S in place, and S as operand tiles
             tc_fence_after();
-            const float last = f[C - 1];
-            tmem_ld32(lb + TM_S, r);
-            tmem_wait_ld();
+            if constexpr (BWD) tmem_get(lb + TM_S, x);
+            else tmem_get_sum(lb + TM_S, x);
+#pragma unroll
+            for (int e = 0; e < NPAIR; ++e) {
+                const float2 d = mul2(f2(last, last), x[e]);
+                y[2 * e] = __float_as_uint(d.x);
+                y[2 * e + 1] = __float_as_uint(d.y);
+            }
+            tmem_store(lb + TM_S, y);
+            if constexpr (!BWD) tmem_store(lb + TM_S + 64, zeros);
             if (states) {
                 if constexpr (BWD) {
-                    round_row(r, hi);
+                    round_row(x, hi);
                 } else {
-                    split_row(r, hi, lo);
-                    put_row(smem + L::SL, t, half, lo);
+                    split_row(x, hi, lo);
+                    put_row(smem + L::SL, t, part, lo);
                 }
-                put_row(smem + L::SH, t, half, hi);
+                put_row(smem + L::SH, t, part, hi);
             }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(last * __uint_as_float(r[e]));
-            tmem_st32(lb + TM_S, r);
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(bar(B_S));
-            // the state at the chunk's start (its end, backward), [tile][n][64 p] bf16, as the tile's image
-            void* keep = BWD ? p.dstates : p.states;
-            if (keep && states) put_row(static_cast<unsigned char*>(keep) + (rec * tiles + pt) * (DK * PT * 2), t, half, hi);
-
+            arrive(B_S);
             if (!krows) {
                 if constexpr (BWD) {
                     // scale e^c do, rows 64-127 of the stacked operand of product 3
                     // (whose previous contents product 3 of the last chunk has read)
-                    const float e = p.scale * f[i];
+                    const float e = p.scale * eg;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint4 d = *reinterpret_cast<const uint4*>(slot + L::V + tile_off<128>(i, 4 * half + x));
-                        *reinterpret_cast<uint4*>(smem + L::XL + tile_off<128>(i, 4 * half + x)) =
+                    for (int k = 0; k < CW / 8; ++k) {
+                        const uint4 d = *reinterpret_cast<const uint4*>(slot + L::V + tile_off<128>(i, CW / 8 * part + k));
+                        *reinterpret_cast<uint4*>(smem + L::XL + tile_off<128>(i, CW / 8 * part + k)) =
                             make_uint4(pack_bf16x2(bf16_lo(d.x) * e, bf16_hi(d.x) * e), pack_bf16x2(bf16_lo(d.y) * e, bf16_hi(d.y) * e),
                                        pack_bf16x2(bf16_lo(d.z) * e, bf16_hi(d.z) * e), pack_bf16x2(bf16_lo(d.w) * e, bf16_hi(d.w) * e));
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(bar(B_DO));
+                    arrive(B_DO);
+                    arrive(B_EMPTY + (c & 1));
                 } else {
+                    arrive(B_EMPTY + (c & 1));
                     if (c > 0) {
                         if (!(ok = wwait(B_P4, c - 1))) break;
                         tc_fence_after();
-                        put_o(chunk_of(c - 1));
+                        put_o();
                     }
-                    const float e = p.scale * f[i];
                     if (!(ok = wwait(B_P1, c))) break;
                     tc_fence_after();
-                    tmem_ld32(lb + TM_X, r);
-                    tmem_wait_ld();
+                    tmem_get_sum(lb + TM_X, qs);
                     tc_fence_before();
+                    const float e = p.scale * eg;
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) qs[x] = e * __uint_as_float(r[x]);
+                    for (int k = 0; k < NPAIR; ++k) qs[k] = mul2(f2(e, e), qs[k]);
                 }
-                mbar_arrive(bar(B_EMPTY + (c & 1)));
                 continue;
             }
-            const float eg = f[i], tail = f[C + i], beta = f[2 * C + i];
             if constexpr (!BWD) {
-                uint4 vv[4];
+                float2 bv[NPAIR];                                // beta v, before the product is there
 #pragma unroll
-                for (int x = 0; x < 4; ++x) vv[x] = *reinterpret_cast<const uint4*>(slot + L::V + tile_off<128>(i, 4 * half + x));
+                for (int k = 0; k < CW / 8; ++k) {
+                    const uint4 d = *reinterpret_cast<const uint4*>(slot + L::V + tile_off<128>(i, CW / 8 * part + k));
+                    const uint32_t w4[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bv[4 * k + e] = mul2(f2(beta, beta), f2(bf16_lo(w4[e]), bf16_hi(w4[e])));
+                }
+                const float nb = -beta * eg;
                 if (!(ok = wwait(B_P1, c))) break;
                 tc_fence_after();
-                tmem_ld32(lb + TM_X, r);
-                tmem_wait_ld();
+                tmem_get_sum(lb + TM_X, x);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t v4[4] = {vv[x].x, vv[x].y, vv[x].z, vv[x].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int k = 8 * x + 2 * e;
-                        r[k] = __float_as_uint(beta * fmaf(-eg, __uint_as_float(r[k]), bf16_lo(v4[e])));
-                        r[k + 1] = __float_as_uint(beta * fmaf(-eg, __uint_as_float(r[k + 1]), bf16_hi(v4[e])));
-                    }
-                }
-                split_row(r, hi, lo);
-                put_row(smem + L::XH, i, half, hi);
-                put_row(smem + L::XL, i, half, lo);
+                for (int e = 0; e < NPAIR; ++e) x[e] = fma2(f2(nb, nb), x[e], bv[e]);
+                split_row(x, hi, lo);
+                put_row(smem + L::XH, i, part, hi);
+                put_row(smem + L::XL, i, part, lo);
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(bar(B_X));
-                mbar_arrive(bar(B_EMPTY + (c & 1)));
+                arrive(B_X);
+                arrive(B_EMPTY + (c & 1));
                 if (!(ok = wwait(B_P2, c))) break;
                 tc_fence_after();
-                tmem_ld32(lb + TM_U, r);
-                tmem_wait_ld();
-                uint32_t u[16];
-                round_row(r, u);
+                tmem_get_sum(lb + TM_U, x);
+                uint32_t u[NPAIR];
+                round_row(x, u);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(tail * __uint_as_float(r[e]));
-                split_row(r, hi, lo);
-                put_row(smem + L::XH, i, half, hi);          // product 2 has read x
-                put_row(smem + L::XL, i, half, lo);
-                put_row(smem + L::U, i, half, u);
+                for (int e = 0; e < NPAIR; ++e) x[e] = mul2(f2(tail, tail), x[e]);
+                split_row(x, hi, lo);
+                put_row(smem + L::XH, i, part, hi);          // product 2 has read x
+                put_row(smem + L::XL, i, part, lo);
+                put_row(smem + L::U, i, part, u);
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(bar(B_V));
-                if (p.u) put_row(static_cast<unsigned char*>(p.u) + (rec * tiles + pt) * (C * PT * 2), i, half, u);
+                arrive(B_V);
             } else {
                 if (!(ok = wwait(B_P1, c))) break;           // product 0 came before it
                 tc_fence_after();
-                uint32_t d[32];
-                tmem_ld32(lb + TM_X, r);
-                tmem_ld32(lb + TM_O, d);
+                uint32_t a[CW], d[CW];
+                tmem_issue(lb + TM_X, a);
+                tmem_issue(lb + TM_O, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fmaf(tail, __uint_as_float(r[e]), __uint_as_float(d[e])));
-                round_row(r, hi);
-                put_row(smem + L::XH, i, half, hi);
+                for (int e = 0; e < NPAIR; ++e)
+                    x[e] = fma2(f2(tail, tail), f2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
+                                f2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+                round_row(x, hi);
+                put_row(smem + L::XH, i, part, hi);
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(bar(B_X));
-                mbar_arrive(bar(B_EMPTY + (c & 1)));
+                arrive(B_X);
+                arrive(B_EMPTY + (c & 1));
                 if (!(ok = wwait(B_P2, c))) break;
                 tc_fence_after();
-                tmem_ld32(lb + TM_U, r);
-                tmem_wait_ld();
-                const float neg = -beta * eg;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    hi[e] = pack_bf16x2(neg * __uint_as_float(r[2 * e]), neg * __uint_as_float(r[2 * e + 1]));
-                put_row(smem + L::XH, i, half, hi);          // product 2 has read x
+                tmem_get(lb + TM_U, x);
+                round_row(x, -beta * eg, hi);
+                put_row(smem + L::XH, i, part, hi);          // product 2 has read x
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(bar(B_V));
-                round_row(r, lo);                            // r, and dv = beta r
-                put_row(static_cast<unsigned char*>(p.dr) + (rec * tiles + pt) * (C * PT * 2), i, half, lo);
-                if (ch * C + i < p.seqlen) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        hi[e] = pack_bf16x2(beta * __uint_as_float(r[2 * e]), beta * __uint_as_float(r[2 * e + 1]));
-                    uint4* o = reinterpret_cast<uint4*>(static_cast<bf16*>(p.dv) + ((b * p.seqlen + ch * C + i) * p.nheads + h) * p.headdim + pt * PT + 32 * half);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-                }
+                arrive(B_V);
+                round_row(x, lo);                      // r, and dv = beta r
+                put_row(smem + L::U, i, part, lo);
+                round_row(x, beta, hi);
+                put_row(smem + L::OUT, i, part, hi);
+                fence_proxy_async_smem();
+                arrive(B_OUT);
             }
         }
         if constexpr (!BWD) {
-            if (ok && !krows && (ok = wwait(B_P4, n - 1))) {
+            if (ok && !krows && (ok = wwait(B_STORED, n - 1) && wwait(B_P4, n - 1))) {
                 tc_fence_after();
-                put_o(chunk_of(n - 1));
+                put_o();
             }
         }
         float* sT = BWD ? p.dh0 : p.hT;
         if (ok && sT && states && wwait(B_P3, n - 1)) {
             tc_fence_after();
-            tmem_ld32(lb + TM_S, r);
-            tmem_wait_ld();
+            if constexpr (BWD) tmem_get(lb + TM_S, x);
+            else tmem_get_sum(lb + TM_S, x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sT[sbase + (int64_t)e * DK] = __uint_as_float(r[e]);
+            for (int e = 0; e < NPAIR; ++e) {
+                sT[sbase + (int64_t)(2 * e) * DK] = x[e].x;
+                sT[sbase + (int64_t)(2 * e + 1) * DK] = x[e].y;
+            }
         }
     }
     tc_fence_before();
@@ -447,14 +594,15 @@ cudaError_t map_steps(CUtensorMap* m, const void* base, int64_t width, int64_t h
 
 template <int DK, bool BWD>
 cudaError_t launch(const GDRArgs& a, cudaStream_t s) {
-    CUtensorMap mk, mq, mv;
+    CUtensorMap mk, mq, mv, mo;
     cudaError_t e;
     if ((e = map_steps(&mk, a.k, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mq, a.q, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mv, BWD ? a.dout : a.v, a.headdim, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
+    if ((e = map_steps(&mo, BWD ? a.dv : a.o, a.headdim, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
     constexpr int bytes = Smem<DK>::BYTES;
     if ((e = cudaFuncSetAttribute(gdr_chain_kernel<DK, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    gdr_chain_kernel<DK, BWD><<<(unsigned)(a.batch * a.nheads * (a.headdim / PT)), NTHREADS, bytes, s>>>(mk, mq, mv, a);
+    gdr_chain_kernel<DK, BWD><<<(unsigned)(a.batch * a.nheads * (a.headdim / PT)), NTHREADS, bytes, s>>>(mk, mq, mv, mo, a);
     return cudaGetLastError();
 }
 
