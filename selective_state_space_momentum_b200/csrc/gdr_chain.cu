@@ -40,7 +40,6 @@
 #include <cuda.h>
 
 #include "gdr_common.cuh"
-#include "mm_tma_host.h"
 
 namespace mmscan {
 
@@ -71,39 +70,6 @@ struct Smem {
     static_assert(BYTES <= 227 * 1024 && SLOT % 1024 == 0 && SH % 1024 == 0 && XH % 1024 == 0, "shared memory");
 };
 
-// `bytes` (a multiple of 16) of consecutive global memory into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
-// `bytes` of shared memory to consecutive global memory (this thread's bulk group).
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" :: "l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-
-// mbar_wait for waits on the critical path: a try may sleep in hardware for up
-// to 20 us (a polling warp takes issue slots and shared-memory cycles from the
-// ones that work), and the limit's clock is read only between tries.
-__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, unsigned int* err) {
-    unsigned long long t0 = 0;
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
-        if (ok) return true;
-        const unsigned long long now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
-            atomicOr(err, kDevErrTimeout);
-            return false;
-        }
-    }
-}
-
 // One product step and the commit, by the elected lane (always the same) of a
 // warp that runs together: the operands stay in uniform registers (23 cycles a
 // step to issue, against 52 from a single lane's branch).
@@ -118,14 +84,6 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
                  :: "r"(bar) : "memory");
 }
 
-// 16 consecutive 32-bit TMEM columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
 // Two fp32 operations an instruction.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     unsigned long long r;
@@ -145,8 +103,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 // This thread's CW columns from `taddr` on; the sum of the two halves of a
 // product (64 columns apart).
-__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&a)[16]) { tmem_ld16(taddr, a); }
-__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&a)[32]) { tmem_ld32(taddr, a); }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&a)[CW]) {
 #pragma unroll
     for (int k = 0; k < CW; k += 16) {
@@ -158,15 +114,15 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&a)[C
 }
 __device__ __forceinline__ void tmem_get(uint32_t taddr, float2 (&x)[NPAIR]) {
     uint32_t a[CW];
-    tmem_issue(taddr, a);
+    tmem_ld32(taddr, a);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < NPAIR; ++e) x[e] = f2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
 }
 __device__ __forceinline__ void tmem_get_sum(uint32_t taddr, float2 (&x)[NPAIR]) {
     uint32_t a[CW], b[CW];
-    tmem_issue(taddr, a);
-    tmem_issue(taddr + 64, b);
+    tmem_ld32(taddr, a);
+    tmem_ld32(taddr + 64, b);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < NPAIR; ++e)
@@ -523,8 +479,8 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (!(ok = wwait(B_P1, c))) break;           // product 0 came before it
                 tc_fence_after();
                 uint32_t a[CW], d[CW];
-                tmem_issue(lb + TM_X, a);
-                tmem_issue(lb + TM_O, d);
+                tmem_ld32(lb + TM_X, a);
+                tmem_ld32(lb + TM_O, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < NPAIR; ++e)
@@ -576,20 +532,6 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, TM_COLS);
     }
-}
-
-// 4-D bf16 map of a (batch, L, heads, width) tensor, boxes of 64 steps x 64
-// columns of one head, 128-byte swizzle; steps past L read as zeros.
-cudaError_t map_steps(CUtensorMap* m, const void* base, int64_t width, int64_t heads, int64_t L, int64_t batch) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)batch};
-    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)(width * heads) * 2, (cuuint64_t)(width * heads * L) * 2};
-    const cuuint32_t box[4] = {64, 1, C, 1}, estr[4] = {1, 1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int DK, bool BWD>

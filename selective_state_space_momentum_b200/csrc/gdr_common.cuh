@@ -4,6 +4,7 @@
 
 #include "mm_common.cuh"
 #include "mm_internal.h"
+#include "mm_tma_host.h"
 
 namespace mmscan {
 namespace gdr {
@@ -145,6 +146,53 @@ __device__ __forceinline__ void load_tile(unsigned char* tile, const void* src, 
         const bool in = r < valid;
         cp_async_16(tile + tile_off<RB>(r, c), static_cast<const unsigned char*>(src) + (in ? r : 0) * stride + c * 16, in ? 16 : 0);
     }
+}
+
+// `bytes` (a multiple of 16) of consecutive global memory into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// `bytes` of shared memory to consecutive global memory (this thread's bulk group).
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" :: "l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+// mbar_wait for waits on the critical path: a try may sleep in hardware for up
+// to 20 us (a polling warp takes issue slots and shared-memory cycles from the
+// ones that work), and the limit's clock is read only between tries.
+__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, unsigned int* err) {
+    unsigned long long t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
+        if (ok) return true;
+        const unsigned long long now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            atomicOr(err, kDevErrTimeout);
+            return false;
+        }
+    }
+}
+
+// 4-D bf16 map of a (batch, L, heads, width) tensor, boxes of 64 steps x 64
+// columns of one head, 128-byte swizzle; steps past L read as zeros.
+inline cudaError_t map_steps(CUtensorMap* m, const void* base, int64_t width, int64_t heads, int64_t L, int64_t batch) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)(width * heads) * 2, (cuuint64_t)(width * heads * L) * 2};
+    const cuuint32_t box[4] = {64, 1, C, 1}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace gdr
