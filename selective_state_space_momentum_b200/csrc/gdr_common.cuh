@@ -74,19 +74,13 @@ __device__ __forceinline__ void load_a_km(uint32_t tile, int k0, int mc, int lan
     ldsm4t(tile + tile_off<RB>(k0 + (m >> 1) * 8 + (lane & 7), mc + (m & 1)), r);
 }
 
-// The A operand of k-step kt from accumulators c (the product before it).
-template <int NT>
-__device__ __forceinline__ void acc_to_a(const float (&c)[NT][4], int kt, uint32_t (&a)[4]) {
-    a[0] = pack_bf16x2(c[2 * kt][0], c[2 * kt][1]);
-    a[1] = pack_bf16x2(c[2 * kt][2], c[2 * kt][3]);
-    a[2] = pack_bf16x2(c[2 * kt + 1][0], c[2 * kt + 1][1]);
-    a[3] = pack_bf16x2(c[2 * kt + 1][2], c[2 * kt + 1][3]);
-}
-// The same split in two bf16 terms: hi + lo is the fp32 value to 2^-17.
+// fp32 values in two bf16 terms: hi + lo is the fp32 value to 2^-17.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16x2(x, y);
     lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
 }
+// The A operand of k-step kt from accumulators c (the product before it), in
+// two terms.
 template <int NT>
 __device__ __forceinline__ void acc_to_a2(const float (&c)[NT][4], int kt, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     split2(c[2 * kt][0], c[2 * kt][1], hi[0], lo[0]);
@@ -129,23 +123,6 @@ template <int RB>
 __device__ __forceinline__ void store_a_km(uint32_t tile, int k0, int mc, int lane, const uint32_t (&r)[4]) {
     const int m = lane >> 3;
     stsm4t(tile + tile_off<RB>(k0 + (m >> 1) * 8 + (lane & 7), mc + (m & 1)), r[0], r[1], r[2], r[3]);
-}
-
-// `bytes` of a tile image from global memory to shared memory, piece by piece.
-__device__ __forceinline__ void load_image(unsigned char* dst, const void* src, int bytes, int tid, int nthreads) {
-    for (int i = tid * 16; i < bytes; i += nthreads * 16) cp_async_16(dst + i, static_cast<const unsigned char*>(src) + i, 16);
-}
-
-// ROWS rows of PIECES x 16 bytes from global memory (row stride `stride`
-// bytes) into a tile of RB-byte rows, by all `nthreads` threads; rows from
-// `valid` on become zeros.
-template <int RB, int ROWS, int PIECES = RB / 16>
-__device__ __forceinline__ void load_tile(unsigned char* tile, const void* src, int64_t stride, int valid, int tid, int nthreads) {
-    for (int i = tid; i < ROWS * PIECES; i += nthreads) {
-        const int r = i / PIECES, c = i % PIECES;
-        const bool in = r < valid;
-        cp_async_16(tile + tile_off<RB>(r, c), static_cast<const unsigned char*>(src) + (in ? r : 0) * stride + c * 16, in ? 16 : 0);
-    }
 }
 
 // `bytes` (a multiple of 16) of consecutive global memory into shared memory.

@@ -178,12 +178,12 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArg
 }
 
 // Resident blocks an SM that the backward's grid counts on: 24 warps at 8
-// elements a thread (up to 80 registers), 16 at 16 (128 registers; a block of
-// 1024 threads has 64 and spills).
-constexpr int norm_bwd_resident(int bt, int elems) { return bt >= 512 ? 1 : elems > 8 ? 512 / bt : 768 / bt; }
+// elements a thread in 16-byte pieces (up to 80 registers); 16 by element or
+// at 16 elements (128 registers; a block of 1024 threads has 64 and spills).
+constexpr int norm_bwd_resident(int bt, int elems, int vec) { return bt >= 512 ? 1 : elems > 8 || vec == 1 ? 512 / bt : 768 / bt; }
 
 template <typename IO, int VEC, int TPR, int NV, bool GATE>
-__global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(TPR), NV * VEC)) norm_bwd_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(TPR), NV * VEC, VEC)) norm_bwd_kernel(const NormArgs p) {
     constexpr int BT = norm_block(TPR);
     constexpr int RPB = BT / TPR;
     __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
@@ -218,8 +218,10 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(
         }
     };
     int64_t r0 = (int64_t)blockIdx.x * RPB;
-    fetch(r0);
+    constexpr bool kAhead = VEC > 1 || (NV <= 8 && TPR < 1024);   // elements one by one: as registers allow
+    if (kAhead) fetch(r0);
     for (; r0 < p.rows; r0 += step) {
+        if (!kAhead) fetch(r0);
         const bool active = r0 + grp < p.rows;
         const int64_t base = (r0 + grp) * cols;
         const float rs = rstd;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(
                 s.y = fmaf(d[k], xh[k], s.y);
             }
         }
-        if (r0 + step < p.rows) fetch(r0 + step);
+        if (kAhead && r0 + step < p.rows) fetch(r0 + step);
         s = row_sum<TPR>(s, red, slot);
         const float a0 = p.rms ? 0.0f : s.x * p.inv_cols;
         const float a1 = s.y * p.inv_cols;
@@ -362,7 +364,7 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
 
 template <typename IO, int VEC, int TPR, int NV>
 cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s) {
-    const int blocks = norm_bwd_blocks(a.rows, a.cols);
+    const int blocks = norm_bwd_blocks(a.rows, a.cols, sizeof(IO) == 4 ? 0 : 1);
     if (a.z) norm_bwd_kernel<IO, VEC, TPR, NV, true><<<blocks, norm_block(TPR), 0, s>>>(a);
     else norm_bwd_kernel<IO, VEC, TPR, NV, false><<<blocks, norm_block(TPR), 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
@@ -376,7 +378,14 @@ cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s) {
 // 8, 65 at 64 (a warp a row); 84 for a grid that stays and walks the rows.
 template <typename IO, int VEC>
 cudaError_t launch_fwd_vec(const NormArgs& a, cudaStream_t s) {
+    if (a.cols <= 8) return launch_fwd<IO, VEC, 1, 8 / VEC>(a, s);
+    if (a.cols <= 16) return launch_fwd<IO, VEC, 2, 8 / VEC>(a, s);
+    if (a.cols <= 32) return launch_fwd<IO, VEC, 4, 8 / VEC>(a, s);
     if (a.cols <= 64) return launch_fwd<IO, VEC, 8, 8 / VEC>(a, s);
+    if constexpr (VEC == 1) {                                // rows no whole number of pieces
+        if (a.cols <= 128) return launch_fwd<IO, 1, 32, 4>(a, s);
+        if (a.cols > 256 && a.cols <= 512) return launch_fwd<IO, 1, 128, 4>(a, s);
+    }
     if (a.cols <= 256) return launch_fwd<IO, VEC, 32, 8 / VEC>(a, s);
     if (a.cols <= 512) return launch_fwd<IO, VEC, 32, 16 / VEC>(a, s);
     if (a.cols <= 2048) return launch_fwd<IO, VEC, 128, 16 / VEC>(a, s);
@@ -385,31 +394,56 @@ cudaError_t launch_fwd_vec(const NormArgs& a, cudaStream_t s) {
     return launch_fwd<IO, VEC, 1024, 16 / VEC>(a, s);
 }
 
-// Backward: threads of a row at 8 elements each, 16 past 2048 columns.
-int norm_bwd_tpr(int64_t cols) {
-    return cols <= 64 ? 8 : cols <= 256 ? 32 : cols <= 1024 ? 128 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
+// Backward: threads of a row at 8 elements each; at 16 past 2048 columns in
+// 16-byte pieces, past 8192 by element.
+int norm_bwd_tpr(int64_t cols, int vec) {
+    if (cols <= 64) return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
+    if (cols <= 2048) return cols <= 256 ? 32 : cols <= 1024 ? 128 : 256;
+    if (vec == 1) return cols <= 4096 ? 512 : 1024;
+    return cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
 }
+int norm_bwd_elems(int64_t cols, int vec) { return cols <= (vec == 1 ? 8192 : 2048) ? 8 : 16; }
 
 template <typename IO, int VEC>
 cudaError_t launch_bwd_vec(const NormArgs& a, cudaStream_t s) {
-    switch (norm_bwd_tpr(a.cols)) {
+    const bool eight = norm_bwd_elems(a.cols, VEC) == 8;
+    switch (norm_bwd_tpr(a.cols, VEC)) {
+        case 1: return launch_bwd<IO, VEC, 1, 8 / VEC>(a, s);
+        case 2: return launch_bwd<IO, VEC, 2, 8 / VEC>(a, s);
+        case 4: return launch_bwd<IO, VEC, 4, 8 / VEC>(a, s);
         case 8: return launch_bwd<IO, VEC, 8, 8 / VEC>(a, s);
-        case 32: return launch_bwd<IO, VEC, 32, 8 / VEC>(a, s);
-        case 128: return launch_bwd<IO, VEC, 128, 8 / VEC>(a, s);
-        case 256: return a.cols <= 2048 ? launch_bwd<IO, VEC, 256, 8 / VEC>(a, s) : launch_bwd<IO, VEC, 256, 16 / VEC>(a, s);
-        case 512: return launch_bwd<IO, VEC, 512, 16 / VEC>(a, s);
-        default: return launch_bwd<IO, VEC, 1024, 16 / VEC>(a, s);
+        case 32:
+            if constexpr (VEC == 1)
+                if (a.cols <= 128) return launch_bwd<IO, 1, 32, 4>(a, s);
+            return launch_bwd<IO, VEC, 32, 8 / VEC>(a, s);
+        case 128:
+            if constexpr (VEC == 1)
+                if (a.cols <= 512) return launch_bwd<IO, 1, 128, 4>(a, s);
+            return launch_bwd<IO, VEC, 128, 8 / VEC>(a, s);
+        case 256:
+            if (eight) return launch_bwd<IO, VEC, 256, 8 / VEC>(a, s);
+            if constexpr (VEC > 1) return launch_bwd<IO, VEC, 256, 16 / VEC>(a, s);
+            break;
+        case 512:
+            if constexpr (VEC == 1) return launch_bwd<IO, 1, 512, 8>(a, s);
+            else return launch_bwd<IO, VEC, 512, 16 / VEC>(a, s);
+        default:
+            if constexpr (VEC == 1)
+                if (eight) return launch_bwd<IO, 1, 1024, 8>(a, s);
+            return launch_bwd<IO, VEC, 1024, 16 / VEC>(a, s);
     }
+    return cudaErrorInvalidConfiguration;
 }
 
 }  // namespace
 
 // Blocks of the backward: what 148 SMs hold at once, and no more than there
 // are rows.
-int norm_bwd_blocks(int64_t rows, int64_t cols) {
-    const int tpr = norm_bwd_tpr(cols), bt = norm_block(tpr);
+int norm_bwd_blocks(int64_t rows, int64_t cols, int io) {
+    const int full = io == 0 ? 4 : 8, vec = cols % full == 0 ? full : 1;
+    const int tpr = norm_bwd_tpr(cols, vec), bt = norm_block(tpr);
     const int64_t need = (rows + bt / tpr - 1) / (bt / tpr);
-    const int64_t fill = 148 * norm_bwd_resident(bt, cols <= 2048 ? 8 : 16);
+    const int64_t fill = 148 * norm_bwd_resident(bt, norm_bwd_elems(cols, vec), vec);
     return (int)(need < fill ? need : fill);
 }
 

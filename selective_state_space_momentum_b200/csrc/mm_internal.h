@@ -291,7 +291,7 @@ struct NormArgs {
 };
 
 constexpr int64_t kNormMaxCols = 16384;
-int norm_bwd_blocks(int64_t rows, int64_t cols);
+int norm_bwd_blocks(int64_t rows, int64_t cols, int io);
 cudaError_t launch_norm_fwd(const NormArgs& a, int io, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int io, cudaStream_t s);
 

@@ -135,7 +135,7 @@ mm_status check_norm(const mm_norm_dims* d, int64_t* io_bytes) {
     return MM_OK;
 }
 
-int64_t norm_ws_bytes(const mm_norm_dims* d) { return (int64_t)mmscan::norm_bwd_blocks(d->rows, d->cols) * 2 * d->cols * 4; }
+int64_t norm_ws_bytes(const mm_norm_dims* d) { return (int64_t)mmscan::norm_bwd_blocks(d->rows, d->cols, d->io) * 2 * d->cols * 4; }
 
 }  // namespace
 
