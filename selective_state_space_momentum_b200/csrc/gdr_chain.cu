@@ -54,7 +54,7 @@ constexpr int CW = 32;                     // columns a thread
 constexpr int EPI_WARPS = 4 * PT / CW, NTHREADS = 32 * EPI_WARPS + 96, W_PROD = EPI_WARPS, W_MMA = W_PROD + 1, W_STORE = W_PROD + 2;
 constexpr int NPAIR = CW / 2;
 constexpr uint32_t TM_S = 0, TM_X = 128, TM_U = 256, TM_O = 384, TM_COLS = 512;   // S, X, U: two halves of 64, forward
-enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_P1 = 5, B_X = 6, B_P2 = 7, B_V = 8, B_P3 = 9, B_P4 = 10, B_OFREE = 11, B_DO = 12, B_OUT = 13, B_STORED = 14, NBAR = 15 };
+enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_P1 = 5, B_X = 6, B_P2 = 7, B_V = 8, B_P3 = 9, B_P4 = 10, B_OFREE = 11, B_DO = 12, B_OUT = 13, B_SST = 14, B_OST = 15, B_UST = 16, NBAR = 17 };
 
 // Shared memory: a ring of two slots (the stacked k and q, [T; Pm], T's low
 // part, v or do, the decays), then the operand tiles the epilogues write.
@@ -188,7 +188,9 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(B_OFREE), EPI_WARPS / 2);
         mbar_init(bar(B_DO), EPI_WARPS / 2);
         mbar_init(bar(B_OUT), EPI_WARPS / 2);
-        mbar_init(bar(B_STORED), 1);
+        mbar_init(bar(B_SST), 1);
+        mbar_init(bar(B_OST), 1);
+        mbar_init(bar(B_UST), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -294,13 +296,17 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
     } else if (warp == W_STORE) {
         // Per chunk: the state's tile, then o of the chunk before and u (backward:
-        // r and dv).  B_STORED: the tiles may be written again.
+        // dv and r); after each, that its tile may be written again (a store
+        // queues behind the loads, so nobody waits for more than it needs).
         if (lane == 0) {
             unsigned char* states = static_cast<unsigned char*>(BWD ? p.dstates : p.states);
             unsigned char* rows = static_cast<unsigned char*>(BWD ? p.dr : p.u);
             const int64_t first = bh * p.nchunks;
             auto store_out = [&](int c) {
                 tma_store_4d(&tm_o, base + L::OUT, pt * PT, (int)h, (int)(chunk_of(c) * C), (int)b);
+                bulk_commit_group();
+                bulk_wait_read_all();
+                mbar_arrive(bar(B_OST));
             };
             bool live = true;
             for (int c = 0; c < n; ++c) {
@@ -308,31 +314,24 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (states) {
                     if (!(live = wait(B_S, c))) break;
                     bulk_store(states + tile * (DK * PT * 2), base + L::SH, DK * PT * 2);
-                }
-                if constexpr (BWD) {
-                    if (!(live = wait(B_OUT, c))) break;
-                    store_out(c);
-                    bulk_store(rows + tile * (C * PT * 2), base + L::U, C * PT * 2);
-                } else {
-                    if (c > 0) {
-                        if (!(live = wait(B_OUT, c - 1))) break;
-                        store_out(c - 1);
-                    }
-                    if (rows) {
-                        if (!(live = wait(B_V, c))) break;
-                        bulk_store(rows + tile * (C * PT * 2), base + L::U, C * PT * 2);
-                    }
-                }
-                bulk_commit_group();
-                bulk_wait_read_all();
-                mbar_arrive(bar(B_STORED));
-            }
-            if constexpr (!BWD) {
-                if (live && wait(B_OUT, n - 1)) {
-                    store_out(n - 1);
                     bulk_commit_group();
+                    bulk_wait_read_all();
+                    mbar_arrive(bar(B_SST));
                 }
+                if (!BWD && c > 0) {
+                    if (!(live = wait(B_OUT, c - 1))) break;
+                    store_out(c - 1);
+                }
+                if (rows) {
+                    if (!(live = wait(BWD ? B_OUT : B_V, c))) break;
+                    bulk_store(rows + tile * (C * PT * 2), base + L::U, C * PT * 2);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                    mbar_arrive(bar(B_UST));
+                }
+                if (BWD) store_out(c);
             }
+            if (!BWD && live && wait(B_OUT, n - 1)) store_out(n - 1);
             bulk_wait_all();                               // complete before the CTA exits
         }
     } else {
@@ -375,13 +374,15 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             arrive(B_OUT);
         };
 
+        const bool keeps = BWD || p.states;                // the state's and the rows' tiles are stored
         bool ok = true;
         for (int c = 0; c < n; ++c) {
             const unsigned char* slot = smem + (c & 1) * L::SLOT;
             const float* f = reinterpret_cast<const float*>(slot + L::F);
             if (!(ok = wwait(B_FULL + (c & 1), c >> 1))) break;
             const float last = f[C - 1], eg = f[i], tail = f[C + i], beta = f[2 * C + i];
-            if (c > 0 && !(ok = wwait(B_STORED, c - 1) && wwait(B_P3, c - 1))) break;
+            if (c > 0 && keeps && !(ok = wwait(B_SST, c - 1))) break;
+            if (c > 0 && !(ok = wwait(B_P3, c - 1))) break;
             // S <- e^(c_last) S in place, and S as operand tiles
             tc_fence_after();
             if constexpr (BWD) tmem_get(lb + TM_S, x);
@@ -425,7 +426,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 } else {
                     arrive(B_EMPTY + (c & 1));
                     if (c > 0) {
-                        if (!(ok = wwait(B_P4, c - 1))) break;
+                        if (!(ok = wwait(B_P4, c - 1) && (c < 2 || wwait(B_OST, c - 2)))) break;
                         tc_fence_after();
                         put_o();
                     }
@@ -461,6 +462,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tc_fence_before();
                 arrive(B_X);
                 arrive(B_EMPTY + (c & 1));
+                if (keeps && c > 0 && !(ok = wwait(B_UST, c - 1))) break;
                 if (!(ok = wwait(B_P2, c))) break;
                 tc_fence_after();
                 tmem_get_sum(lb + TM_U, x);
@@ -492,6 +494,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tc_fence_before();
                 arrive(B_X);
                 arrive(B_EMPTY + (c & 1));
+                if (c > 0 && !(ok = wwait(B_UST, c - 1) && wwait(B_OST, c - 1))) break;
                 if (!(ok = wwait(B_P2, c))) break;
                 tc_fence_after();
                 tmem_get(lb + TM_U, x);
@@ -509,7 +512,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
         }
         if constexpr (!BWD) {
-            if (ok && !krows && (ok = wwait(B_STORED, n - 1) && wwait(B_P4, n - 1))) {
+            if (ok && !krows && (ok = wwait(B_P4, n - 1) && (n < 2 || wwait(B_OST, n - 2)))) {
                 tc_fence_after();
                 put_o();
             }
