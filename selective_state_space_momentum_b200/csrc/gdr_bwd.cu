@@ -39,340 +39,201 @@ namespace gdr {
 namespace {
 
 // ------------------------------------------------- everything else, by chunk ----
+// One CTA a batch row, group and chunk, on tensor cores (tcgen05 / TMEM).  As
+// in the chain, k and q are stacked into one tile of 128 rows, and so are r
+// and do: of every product the rows of k and dk are lanes 0-63, those of q
+// and dq lanes 64-127.  Per head of the group:
+//     1. [k; q] k^T (once)    2. [r; do] u^T     -> [ad; pd], the row and column sums of W
+//     3. ACC += [ad; pd] k    5. ACC += [ad; pd]^T [k; q]  (lanes 0-63; zeros below)
+//     4. Y = [r; do] S        6. Z = u dS'  (lanes 0-63)
+//        dk += tail Z - beta e^c Y, dq += scale e^c Y, and their rows' products with k and q
+// ACC stays in TMEM over the group's heads; what needs a factor of its row
+// (Y, Z) is added in registers, a thread half a row.  Products 4 and 6 run
+// while the epilogue forms [ad; pd].
+//
+// Roles (11 warps): 0-7 the epilogues, then one for the loads and the last
+// stores, one for the products, and one that sums up a head's decays before
+// and its dg and dbeta after.
+//
+// Bound: the latency of one chunk's steps and loads (one CTA an SM: 190 KB of
+// tiles and all of TMEM at P = N = 128).
+constexpr int SLAB = 128 * 128;                        // 64 columns of a stacked tile
+constexpr int GEPI = 8, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
+enum { B_QK = 0, B_RO = 1, B_ST = 2, B_G = 3, B_YZ = 4, B_AP = 5, B_ACC = 6, B_FREE = 7, B_CUM = 8, B_ROWS = 10, B_DONE = 12, NGBAR = 13 };   // B_CUM, B_ROWS: by head parity
+
 template <int DK, int DV>
 struct GradSmem {
-    static constexpr int Q = 0, K = Q + C * DK * 2, DO = K + C * DK * 2, S = DO + C * DV * 2, DS = S + DV * DK * 2;
-    static constexpr int U = DS + DV * DK * 2, R = U + DV * C * 2, PD = R + DV * C * 2, AD = PD + C * C * 2;
-    static constexpr int F = AD + C * C * 2;           // eg, tail, beta
-    static constexpr int CUM = F + 3 * C * 4;          // double c[C]
-    static constexpr int ROW = CUM + C * 8;            // float [4 column groups][3 kinds][C]
-    static constexpr int COL = ROW + 12 * C * 4;       // float [4 row tiles][C]
-    static constexpr int RV = COL + 4 * C * 4;         // float [C]: r.v
-    static constexpr int RED = RV + C * 4;             // float [16]: <S, dS'> by warp
-    static constexpr int BAR = RED + 64;               // q and k; do, u, r, decays; S, dS'
-    static constexpr int BYTES = BAR + 3 * 8;
+    static constexpr int KQ = 0, RO = KQ + DK / 64 * SLAB, U = RO + DV / 64 * SLAB, S = U + DV / 64 * (SLAB / 2);
+    static constexpr int DS = S + DV * DK * 2, V = DS + DV * DK * 2, AP = V + DV / 64 * (SLAB / 2), Z0 = AP + SLAB;
+    static constexpr int F = Z0 + SLAB;                // eg, tail, beta
+    // by head parity: the decays (double c[C], float e^(c - mid), e^(mid - c), [C]) ...
+    static constexpr int CUM = F + 3 * C * 4, CUM_BYTES = C * 8 + 2 * C * 4;
+    // ... and the sums: by column half, of dc by row of [k; q], of e^.. k.(dS' u) and of dbeta by row of k;
+    // the column sums by lane quarter; <S, dS'> by warp
+    static constexpr int ROW = CUM + 2 * CUM_BYTES, ROWS = 2 * 4 * C * 4 + 4 * C * 4 + 64;
+    static constexpr int WIDE = ROW + 2 * ROWS, BAR = WIDE + 16, TSLOT = BAR + NGBAR * 8, ABORT = TSLOT + 8;
+    static constexpr int BYTES = ABORT + 8 + 1024;
+    static_assert(BYTES <= 227 * 1024 && U % 1024 == 0 && S % 1024 == 0 && AP % 1024 == 0, "shared memory");
 };
+constexpr uint32_t TG_KQ = 0, TG_G = 64, TG_ACC = 128, TG_Y = 256, TG_Z = 384;
 
-// acc (16 rows x NTC n-tiles) += A (64 x 64 stored [m][k], or [k][m]) . B stored
-// [k][n] in slabs of 64 columns.
-template <int NTC, bool AKM>
-__device__ __forceinline__ void product(float (&acc)[NTC][4], uint32_t at, uint32_t bt, int m0, int nc0, int k_lo, int k_hi, int lane) {
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        if (kt < k_lo || kt > k_hi) continue;
-        uint32_t a[4];
-        if constexpr (AKM) load_a_km<128>(at, 16 * kt, 2 * m0, lane, a);
-        else load_a_mk<128>(at, 16 * m0, 2 * kt, lane, a);
-#pragma unroll
-        for (int n = 0; n < NTC; n += 2) {
-            uint32_t f[4];
-            load_b_kn<128>(bt + ((nc0 + n) >> 3) * (C * 128), 16 * kt, (nc0 + n) & 7, lane, f);
-            mma(acc[n], a, f[0], f[1]);
-            mma(acc[n + 1], a, f[2], f[3]);
-        }
-    }
-}
-
-// acc += A . B over the head's width: A [row][p], B [n][p], both in tiles of 64 p.
-template <int NTC, int DV, int DK>
-__device__ __forceinline__ void product_p(float (&acc)[NTC][4], uint32_t at, uint32_t bt, int m0, int nc0, int lane) {
-#pragma unroll
-    for (int kt = 0; kt < DV / 16; ++kt) {
-        uint32_t a[4];
-        load_a_mk<128>(at + (kt >> 2) * (C * 128), 16 * m0, 2 * (kt & 3), lane, a);
-#pragma unroll
-        for (int n = 0; n < NTC; n += 2) {
-            uint32_t f[4];
-            load_b_nk<128>(bt + (kt >> 2) * (DK * 128), 8 * (nc0 + n), 2 * (kt & 3), lane, f);
-            mma(acc[n], a, f[0], f[1]);
-            mma(acc[n + 1], a, f[2], f[3]);
-        }
-    }
-}
-
-template <int NTC>
-__device__ __forceinline__ void zero(float (&a)[NTC][4]) {
-#pragma unroll
-    for (int n = 0; n < NTC; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[n][e] = 0.0f;
-}
-
-// Row dots of acc with rows i0 and i0 + 8 of q or k (columns of this warp).
-template <int NTC>
-__device__ __forceinline__ float2 row_dots(const float (&acc)[NTC][4], const unsigned char* tile, int i0, int nc0, int tq) {
-    float2 d = f2(0.0f, 0.0f);
-#pragma unroll
-    for (int n = 0; n < NTC; ++n) {
-        const unsigned char* slab = tile + ((nc0 + n) >> 3) * (C * 128) + 4 * tq;
-        const uint32_t a = *reinterpret_cast<const uint32_t*>(slab + tile_off<128>(i0, (nc0 + n) & 7));
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(slab + tile_off<128>(i0 + 8, (nc0 + n) & 7));
-        d.x = fmaf(acc[n][0], bf16_lo(a), fmaf(acc[n][1], bf16_hi(a), d.x));
-        d.y = fmaf(acc[n][2], bf16_lo(b), fmaf(acc[n][3], bf16_hi(b), d.y));
-    }
-    return d;
-}
-
-// Sixteen warps: warp w the rows 16 (w mod 4) .. and a quarter of the columns.
 template <int DK, int DV>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(GTHREADS, 1)
 gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                    const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dk,
-                    const __grid_constant__ CUtensorMap tm_dq, const GDRArgs p) {
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dq, const GDRArgs p) {
     using L = GradSmem<DK, DV>;
-    constexpr int RB = DK * 2, NTC = DK / 32;
-    extern __shared__ __align__(1024) unsigned char sm[];
+    constexpr int TV = DV / 64, HC = DK / 2;           // tiles of 64 p; columns of q and k a thread
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    unsigned char* sm = smem_raw + (base - raw_addr);
     const int tid = threadIdx.x, lane = tid & 31, w = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int gq = lane >> 2, tq = lane & 3;
-    const int mi = w & 3, hf = w >> 2, nc0 = hf * NTC;
-    const int i0 = 16 * mi + gq;
     const int64_t ch = blockIdx.x % p.nchunks, bg = blockIdx.x / p.nchunks;
     const int64_t b = bg / p.ngroups, grp = bg - b * p.ngroups;
-    const int hpg = (int)(p.nheads / p.ngroups);
+    const int hpg = (int)(p.nheads / p.ngroups), h0 = (int)grp * hpg;
     const int64_t t0 = ch * C;
     const int valid = (int)(p.seqlen - t0 < C ? p.seqlen - t0 : C);
-    const int64_t vstride = p.nheads * DV * 2;
-    const uint32_t base = smem_u32(sm), bar = base + L::BAR;
-    const uint32_t qs = base + L::Q, ks = base + L::K, dos = base + L::DO, ss = base + L::S, dss = base + L::DS, us = base + L::U,
-                   rs = base + L::R, pds = base + L::PD, ads = base + L::AD;
-    float* eg = reinterpret_cast<float*>(sm + L::F);
-    double* cum = reinterpret_cast<double*>(sm + L::CUM);
-    float* rowv = reinterpret_cast<float*>(sm + L::ROW);
-    float* colv = reinterpret_cast<float*>(sm + L::COL);
-    float* rvv = reinterpret_cast<float*>(sm + L::RV);
-    float* red = reinterpret_cast<float*>(sm + L::RED);
-    auto record = [&](int hh) { return (b * p.nheads + grp * hpg + hh) * p.nchunks + ch; };
-    auto issue = [&](int hh) {                // one thread: the tiles of head hh of the group
-        const int64_t rec = record(hh);
-        mbar_expect_tx(bar + 8, 3 * C * DV * 2 + 3 * C * 4);
-#pragma unroll
-        for (int t = 0; t < DV / 64; ++t)
-            tma_load_4d(dos + t * C * 128, &tm_do, bar + 8, 64 * t, (int)grp * hpg + hh, (int)t0, (int)b);
-        bulk_load(us, static_cast<const unsigned char*>(p.u) + rec * DV * C * 2, DV * C * 2, bar + 8);
-        bulk_load(rs, static_cast<const unsigned char*>(p.dr) + rec * DV * C * 2, DV * C * 2, bar + 8);
-        bulk_load(base + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, bar + 8);
-        mbar_expect_tx(bar + 16, 2 * DV * RB);
-        bulk_load(ss, static_cast<const unsigned char*>(p.states) + rec * DV * RB, DV * RB, bar + 16);
-        bulk_load(dss, static_cast<const unsigned char*>(p.dstates) + rec * DV * RB, DV * RB, bar + 16);
-    };
-    // Whether the loads behind barrier k have come (the same answer to everybody).
-    auto landed = [&](int k, int phase) {
-        return __syncthreads_and(mbar_wait_sleep(bar + 8 * k, (uint32_t)phase & 1u, &g_grad_dev_err)) != 0;
-    };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::ABORT);
+    int* wide = reinterpret_cast<int*>(sm + L::WIDE);
+    auto bar = [&](int i) { return base + L::BAR + 8u * (uint32_t)i; };
     if (tid == 0) {
-        for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
+        const int counts[NGBAR] = {1, 1, 1, 1, 1, GEPI, 1, GEPI + 1, 1, 1, GEPI, GEPI, GEPI};
+        for (int i = 0; i < NGBAR; ++i) mbar_init(bar(i), counts[i]);
+        *abort_flag = 0;
         fence_barrier_init();
-        if (!p.stall) {                       // (test only: nothing staged, the waits run out)
-            mbar_expect_tx(bar, 2 * C * RB);
-#pragma unroll
-            for (int s = 0; s < DK / 64; ++s) {
-                tma_load_4d(qs + s * C * 128, &tm_q, bar, 64 * s, (int)grp, (int)t0, (int)b);
-                tma_load_4d(ks + s * C * 128, &tm_k, bar, 64 * s, (int)grp, (int)t0, (int)b);
-            }
-            issue(0);
-        }
     }
+    if (w == 0) tmem_alloc(base + L::TSLOT, 512);
+    for (int i = tid; i < SLAB / 16; i += GTHREADS) *reinterpret_cast<uint4*>(sm + L::Z0 + 16 * i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::TSLOT);
+    auto wait = [&](int i, int phase) -> bool {
+        if (*abort_flag) return false;
+        if (!mbar_wait_sleep(bar(i), (uint32_t)phase & 1u, &g_grad_dev_err)) {
+            *abort_flag = 1;
+            return false;
+        }
+        return true;
+    };
+    auto wwait = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)); };
+    auto arrive = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(i));
+    };
 
-    float dq[NTC][4], dk[NTC][4], qk[2][4], kk[2][4];
-    zero(dq); zero(dk); zero(qk); zero(kk);
-    for (int hh = 0; hh < hpg; ++hh) {
-        const int64_t h = grp * hpg + hh;
-        if (w == 15) {
+    if (w == G_LOAD) {
+        if (lane == 0) {
+            bool live = true;
+            for (int hh = 0; hh < hpg && !p.stall; ++hh) {   // (stall: test only, nothing staged, every wait runs out)
+                if (hh > 0 && !(live = wait(B_FREE, hh - 1))) break;
+                const int h = h0 + hh;
+                const int64_t rec = (b * p.nheads + h) * p.nchunks + ch;
+                if (hh == 0) {
+                    mbar_expect_tx(bar(B_QK), DK / 64 * SLAB);
+#pragma unroll
+                    for (int s = 0; s < DK / 64; ++s) {
+                        tma_load_4d(base + L::KQ + s * SLAB, &tm_k, bar(B_QK), 64 * s, (int)grp, (int)t0, (int)b);
+                        tma_load_4d(base + L::KQ + s * SLAB + SLAB / 2, &tm_q, bar(B_QK), 64 * s, (int)grp, (int)t0, (int)b);
+                    }
+                }
+                mbar_expect_tx(bar(B_RO), TV * 2 * SLAB + 3 * C * 4);
+#pragma unroll
+                for (int t = 0; t < TV; ++t) {
+                    bulk_load(base + L::RO + t * SLAB, static_cast<const unsigned char*>(p.dr) + (rec * TV + t) * (SLAB / 2), SLAB / 2, bar(B_RO));
+                    tma_load_4d(base + L::RO + t * SLAB + SLAB / 2, &tm_do, bar(B_RO), 64 * t, h, (int)t0, (int)b);
+                    tma_load_4d(base + L::V + t * (SLAB / 2), &tm_v, bar(B_RO), 64 * t, h, (int)t0, (int)b);
+                }
+                bulk_load(base + L::U, static_cast<const unsigned char*>(p.u) + rec * TV * (SLAB / 2), TV * (SLAB / 2), bar(B_RO));
+                bulk_load(base + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, bar(B_RO));
+                mbar_expect_tx(bar(B_ST), 2 * DV * DK * 2);
+                bulk_load(base + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * DK * 2, DV * DK * 2, bar(B_ST));
+                bulk_load(base + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * DK * 2, DV * DK * 2, bar(B_ST));
+            }
+            // dq, dk, staged in the tile of k and q (rows past L are clipped)
+            if (live && wait(B_DONE, 0)) {
+#pragma unroll
+                for (int s = 0; s < DK / 64; ++s) {
+                    tma_store_4d(&tm_dk, base + L::KQ + s * SLAB, 64 * s, (int)grp, (int)t0, (int)b);
+                    tma_store_4d(&tm_dq, base + L::KQ + s * SLAB + SLAB / 2, 64 * s, (int)grp, (int)t0, (int)b);
+                }
+                bulk_commit_group();
+            }
+            bulk_wait_all();                                 // complete before the CTA exits
+        }
+    } else if (w == G_MMA) {
+        const uint32_t kq = base + L::KQ, ro = base + L::RO, u = base + L::U, ap = base + L::AP;
+        constexpr uint32_t ID64 = umma_idesc_bf16(128, 64, 0, 0), IDKK = umma_idesc_bf16(128, DK, 0, 0),
+                           IDKN = umma_idesc_bf16(128, DK, 0, 1), IDNN = umma_idesc_bf16(128, DK, 1, 1);
+        auto kmaj = [&](uint32_t tile, int s, uint32_t stride) { return umma_desc_sw128(tile + (s >> 2) * stride + (s & 3) * 32, 16, 1024); };
+        bool live = wwait(B_QK, 0);
+        if (live) {
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s) umma_elect(tmem + TG_KQ, kmaj(kq, s, SLAB), kmaj(kq, s, SLAB), ID64, s > 0);
+        }
+        for (int hh = 0; hh < hpg && live; ++hh) {
+            if (!(live = wwait(B_RO, hh))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_G, kmaj(ro, s, SLAB), kmaj(u, s, SLAB / 2), ID64, s > 0);
+            commit_elect(bar(B_G));
+            if (!(live = wwait(B_ST, hh))) break;
+#pragma unroll
+            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Y, kmaj(ro, s, SLAB), kmaj(base + L::S, s, DK * 128), IDKK, s > 0);
+#pragma unroll
+            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Z, kmaj(u, s, SLAB / 2), kmaj(base + L::DS, s, DK * 128), IDKK, s > 0);
+            commit_elect(bar(B_YZ));
+            if (!(live = wwait(B_AP, hh))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < C / 16; ++s)
+                umma_elect(tmem + TG_ACC, kmaj(ap, s, 0), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDKN, hh > 0 || s > 0);
+#pragma unroll
+            for (int s = 0; s < 2 * C / 16; ++s)
+                umma_elect(tmem + TG_ACC, umma_desc_sw128(ap + s * 2048, L::Z0 - L::AP, 1024), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDNN, 1u);
+            commit_elect(bar(B_ACC));
+            commit_elect(bar(B_FREE));
+        }
+        if (live) wwait(B_ACC, hpg - 1);                     // the last commit must land before the CTA may exit
+    } else if (w == G_AUX) {
+        auto decays = [&](int hh) {
+            double* cum = reinterpret_cast<double*>(sm + L::CUM + (hh & 1) * L::CUM_BYTES);
+            float* ef = reinterpret_cast<float*>(cum + C);
+            const int r = 2 * lane;
             double s0, s1, last;
-            chunk_cumsum(static_cast<const bf16*>(p.g) + (b * p.seqlen + t0) * p.nheads + h, p.nheads, valid, lane, s0, s1, last);
-            cum[2 * lane] = s0;
-            cum[2 * lane + 1] = s1;
-        }
-        if (hh == 0) {                        // q.k and k.k are the group's
-            if (!landed(0, 0)) return;
-            if (hf <= mi) {
-#pragma unroll
-                for (int kt = 0; kt < DK / 16; ++kt) {
-                    const uint32_t slab = (kt >> 2) * C * 128;
-                    uint32_t aq[4], ak[4], f[4];
-                    load_a_mk<128>(qs + slab, 16 * mi, 2 * (kt & 3), lane, aq);
-                    load_a_mk<128>(ks + slab, 16 * mi, 2 * (kt & 3), lane, ak);
-                    load_b_nk<128>(ks + slab, 16 * hf, 2 * (kt & 3), lane, f);
-                    mma(qk[0], aq, f[0], f[1]);
-                    mma(qk[1], aq, f[2], f[3]);
-                    mma(kk[0], ak, f[0], f[1]);
-                    mma(kk[1], ak, f[2], f[3]);
-                }
-            }
-        }
-        if (!landed(1, hh)) return;
-        float dp[2][4], da[2][4];
-        zero(dp); zero(da);
-        if (hf <= mi) {
-#pragma unroll
-            for (int kt = 0; kt < DV / 16; ++kt) {
-                const uint32_t slab = (kt >> 2) * C * 128;
-                uint32_t ao[4], ar[4], f[4];
-                load_a_mk<128>(dos + slab, 16 * mi, 2 * (kt & 3), lane, ao);
-                load_a_mk<128>(rs + slab, 16 * mi, 2 * (kt & 3), lane, ar);
-                load_b_nk<128>(us + slab, 16 * hf, 2 * (kt & 3), lane, f);
-                mma(dp[0], ao, f[0], f[1]);
-                mma(dp[1], ao, f[2], f[3]);
-                mma(da[0], ar, f[0], f[1]);
-                mma(da[1], ar, f[2], f[3]);
-            }
-        }
-        // rows' sums kept by this thread: [row half] of dc, of e^.. k.(dS' u), of dbeta
-        float rc[2] = {0.0f, 0.0f}, rk[2] = {0.0f, 0.0f}, rb[2] = {0.0f, 0.0f};
-        const double c0 = cum[i0], c1 = cum[i0 + 8];
-        const float b0 = eg[2 * C + i0], b1 = eg[2 * C + i0 + 8];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            if (hf > mi) break;
-            const int j = 16 * hf + 8 * n + 2 * tq;
-            float cs[2] = {0.0f, 0.0f};
-            float pv[4], av[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + 8 * (e >> 1), jj = j + (e & 1);
-                const float d = jj <= i ? ex2_approx((float)(((e >> 1 ? c1 : c0) - cum[jj]) * kLog2e)) : 0.0f;
-                pv[e] = p.scale * d * dp[n][e];
-                const float x = jj < i ? -d * da[n][e] : 0.0f;
-                av[e] = (e >> 1 ? b1 : b0) * x;
-                const float wv = jj < i ? fmaf(pv[e], qk[n][e], av[e] * kk[n][e]) : 0.0f;
-                rc[e >> 1] += wv;
-                cs[e & 1] += wv;
-                rb[e >> 1] = fmaf(x, kk[n][e], rb[e >> 1]);
-            }
-            *reinterpret_cast<uint32_t*>(sm + L::PD + tile_off<128>(i0, 2 * hf + n) + 4 * tq) = pack_bf16x2(pv[0], pv[1]);
-            *reinterpret_cast<uint32_t*>(sm + L::PD + tile_off<128>(i0 + 8, 2 * hf + n) + 4 * tq) = pack_bf16x2(pv[2], pv[3]);
-            *reinterpret_cast<uint32_t*>(sm + L::AD + tile_off<128>(i0, 2 * hf + n) + 4 * tq) = pack_bf16x2(av[0], av[1]);
-            *reinterpret_cast<uint32_t*>(sm + L::AD + tile_off<128>(i0 + 8, 2 * hf + n) + 4 * tq) = pack_bf16x2(av[2], av[3]);
-#pragma unroll
-            for (int m = 4; m < 32; m <<= 1) {
-                cs[0] += __shfl_xor_sync(0xffffffffu, cs[0], m);
-                cs[1] += __shfl_xor_sync(0xffffffffu, cs[1], m);
-            }
-            if (gq == 0) *reinterpret_cast<float2*>(colv + mi * C + j) = f2(cs[0], cs[1]);
-        }
-        {                                     // r.v, eight threads a row
-            const int i = tid >> 3, part = tid & 7;
-            float d = 0.0f;
-            if (i < valid) {
-                const uint4* vg = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.v) + (b * p.seqlen + t0 + i) * vstride + h * DV * 2);
-#pragma unroll
-                for (int x = part; x < DV / 8; x += 8) {
-                    const uint4 vv = vg[x];
-                    const uint4 rr = *reinterpret_cast<const uint4*>(sm + L::R + (x >> 3) * (C * 128) + tile_off<128>(i, x & 7));
-                    d = fmaf(bf16_lo(vv.x), bf16_lo(rr.x), fmaf(bf16_hi(vv.x), bf16_hi(rr.x), d));
-                    d = fmaf(bf16_lo(vv.y), bf16_lo(rr.y), fmaf(bf16_hi(vv.y), bf16_hi(rr.y), d));
-                    d = fmaf(bf16_lo(vv.z), bf16_lo(rr.z), fmaf(bf16_hi(vv.z), bf16_hi(rr.z), d));
-                    d = fmaf(bf16_lo(vv.w), bf16_lo(rr.w), fmaf(bf16_hi(vv.w), bf16_hi(rr.w), d));
-                }
-            }
-#pragma unroll
-            for (int m = 1; m < 8; m <<= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-            if (part == 0) rvv[i] = d;
-        }
-        if (!landed(2, hh)) return;           // pd, ad, S, dS' are there
-
-        product<NTC, false>(dq, pds, ks, mi, nc0, 0, mi, lane);
-        product<NTC, true>(dk, pds, qs, mi, nc0, mi, 3, lane);
-        product<NTC, false>(dk, ads, ks, mi, nc0, 0, mi, lane);
-        product<NTC, true>(dk, ads, ks, mi, nc0, mi, 3, lane);
-        float acc[NTC][4];
-        {
-            zero(acc);
-            product_p<NTC, DV, DK>(acc, dos, ss, mi, nc0, lane);
-            const float f0 = p.scale * eg[i0], f1 = p.scale * eg[i0 + 8];
-            const float2 d = row_dots<NTC>(acc, sm + L::Q, i0, nc0, tq);
-            rc[0] = fmaf(f0, d.x, rc[0]);
-            rc[1] = fmaf(f1, d.y, rc[1]);
-#pragma unroll
-            for (int n = 0; n < NTC; ++n) {
-                dq[n][0] = fmaf(f0, acc[n][0], dq[n][0]);
-                dq[n][1] = fmaf(f0, acc[n][1], dq[n][1]);
-                dq[n][2] = fmaf(f1, acc[n][2], dq[n][2]);
-                dq[n][3] = fmaf(f1, acc[n][3], dq[n][3]);
-            }
-        }
-        {
-            zero(acc);
-            product_p<NTC, DV, DK>(acc, rs, ss, mi, nc0, lane);
-            const float f0 = eg[i0], f1 = eg[i0 + 8];
-            const float2 d = row_dots<NTC>(acc, sm + L::K, i0, nc0, tq);
-            rb[0] = fmaf(-f0, d.x, rb[0]);
-            rb[1] = fmaf(-f1, d.y, rb[1]);
-            rc[0] = fmaf(-f0 * b0, d.x, rc[0]);
-            rc[1] = fmaf(-f1 * b1, d.y, rc[1]);
-#pragma unroll
-            for (int n = 0; n < NTC; ++n) {
-                dk[n][0] = fmaf(-f0 * b0, acc[n][0], dk[n][0]);
-                dk[n][1] = fmaf(-f0 * b0, acc[n][1], dk[n][1]);
-                dk[n][2] = fmaf(-f1 * b1, acc[n][2], dk[n][2]);
-                dk[n][3] = fmaf(-f1 * b1, acc[n][3], dk[n][3]);
-            }
-        }
-        {
-            zero(acc);
-            product_p<NTC, DV, DK>(acc, us, dss, mi, nc0, lane);
-            const float f0 = eg[C + i0], f1 = eg[C + i0 + 8];
-            const float2 d = row_dots<NTC>(acc, sm + L::K, i0, nc0, tq);
-            rk[0] = f0 * d.x;
-            rk[1] = f1 * d.y;
-#pragma unroll
-            for (int n = 0; n < NTC; ++n) {
-                dk[n][0] = fmaf(f0, acc[n][0], dk[n][0]);
-                dk[n][1] = fmaf(f0, acc[n][1], dk[n][1]);
-                dk[n][2] = fmaf(f1, acc[n][2], dk[n][2]);
-                dk[n][3] = fmaf(f1, acc[n][3], dk[n][3]);
-            }
-        }
-        // <S, dS'>: both tiles have the same layout
-        float sd = 0.0f;
-#pragma unroll 4
-        for (int i = tid; i < DV * RB / 16; i += 512) {
-            const uint4 x = *reinterpret_cast<const uint4*>(sm + L::S + i * 16), y = *reinterpret_cast<const uint4*>(sm + L::DS + i * 16);
-            sd = fmaf(bf16_lo(x.x), bf16_lo(y.x), fmaf(bf16_hi(x.x), bf16_hi(y.x), sd));
-            sd = fmaf(bf16_lo(x.y), bf16_lo(y.y), fmaf(bf16_hi(x.y), bf16_hi(y.y), sd));
-            sd = fmaf(bf16_lo(x.z), bf16_lo(y.z), fmaf(bf16_hi(x.z), bf16_hi(y.z), sd));
-            sd = fmaf(bf16_lo(x.w), bf16_lo(y.w), fmaf(bf16_hi(x.w), bf16_hi(y.w), sd));
-        }
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
-        if (lane == 0) red[w] = sd;
-#pragma unroll
-        for (int m = 1; m < 4; m <<= 1)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                rc[e] += __shfl_xor_sync(0xffffffffu, rc[e], m);
-                rk[e] += __shfl_xor_sync(0xffffffffu, rk[e], m);
-                rb[e] += __shfl_xor_sync(0xffffffffu, rb[e], m);
-            }
-        if (tq == 0) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                rowv[(hf * 3 + 0) * C + i0 + 8 * e] = rc[e];
-                rowv[(hf * 3 + 1) * C + i0 + 8 * e] = rk[e];
-                rowv[(hf * 3 + 2) * C + i0 + 8 * e] = rb[e];
-            }
-        }
-        const float eg_last = eg[C - 1];
-        __syncthreads();
-        if (tid == 0 && hh + 1 < hpg) issue(hh + 1);       // every product has read this head's tiles
-        if (w == 0) {
+            chunk_cumsum(static_cast<const bf16*>(p.g) + (b * p.seqlen + t0) * p.nheads + h0 + hh, p.nheads, valid, lane, s0, s1, last);
+            cum[r] = s0;
+            cum[r + 1] = s1;
+            // factors of e^(c_i - c_j), or ones (and then by element), as in the preparing kernel
+            const double first = __shfl_sync(0xffffffffu, s0, 0), mid = 0.5 * (first + last);
+            const double a0 = (s0 - mid) * kLog2e, a1 = (s1 - mid) * kLog2e;
+            const bool far = __any_sync(0xffffffffu, !(fabs(a0) < 60.0) || !(fabs(a1) < 60.0));
+            *reinterpret_cast<float2*>(ef + r) = far ? f2(1.0f, 1.0f) : f2(ex2_approx((float)a0), ex2_approx((float)a1));
+            *reinterpret_cast<float2*>(ef + C + r) = far ? f2(1.0f, 1.0f) : f2(ex2_approx((float)-a0), ex2_approx((float)-a1));
+            if (lane == 0) wide[hh & 1] = far;
+            arrive(B_CUM + (hh & 1));
+        };
+        decays(0);
+        for (int hh = 0; hh < hpg; ++hh) {
+            if (hh + 1 < hpg) decays(hh + 1);                // its buffer was head hh - 1's, whose sums are taken
+            if (!wwait(B_ROWS + (hh & 1), hh >> 1)) break;
+            const float* rowc = reinterpret_cast<const float*>(sm + L::ROW + (hh & 1) * L::ROWS);   // [half][128]
+            const float* rowk = rowc + 4 * C;                                                      // [half][C]
+            const float* rowb = rowk + 2 * C;
+            const float* colv = rowb + 2 * C;                                                      // [quarter][C]
+            const float* red = colv + 4 * C;                                                       // [warp], then e^(c_last)
             float dc[2], ok[2], db[2], sums = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                float col = 0.0f;
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (m >= i / 16) col += colv[m * C + i];       // row tiles from the diagonal on were written
-                ok[e] = dc[e] = db[e] = 0.0f;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    dc[e] += rowv[3 * m * C + i];
-                    ok[e] += rowv[(3 * m + 1) * C + i];
-                    db[e] += rowv[(3 * m + 2) * C + i];
-                }
-                dc[e] -= col + ok[e];
+                float col = colv[C + i] + colv[3 * C + i];   // rows 32-63 of k and of q
+                if (i < 32) col += colv[i] + colv[2 * C + i];
+                ok[e] = rowk[i] + rowk[C + i];
+                db[e] = rowb[i] + rowb[C + i];
+                dc[e] = rowc[i] + rowc[2 * C + i] + rowc[C + i] + rowc[3 * C + i] - col - ok[e];
                 sums += ok[e];
             }
 #pragma unroll
@@ -380,8 +241,8 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (lane == 31) {
                 float t = 0.0f;
 #pragma unroll
-                for (int m = 0; m < 16; ++m) t += red[m];
-                dc[1] = fmaf(eg_last, t, dc[1] + sums);
+                for (int m = 0; m < GEPI; ++m) t += red[m];
+                dc[1] = fmaf(red[GEPI], t, dc[1] + sums);
             }
             // dg = the sums from each row to the chunk's end
             dc[0] += dc[1];
@@ -392,39 +253,201 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (lane + m < 32) run += dn;
             }
             const float after = run - dc[0];
-            const int64_t at = (b * p.seqlen + t0 + 2 * lane) * p.nheads + h;
+            const int64_t at = (b * p.seqlen + t0 + 2 * lane) * p.nheads + h0 + hh;
             bf16* dg = static_cast<bf16*>(p.dg);
-            bf16* dbg = static_cast<bf16*>(p.dbeta);
+            bf16* dbeta = static_cast<bf16*>(p.dbeta);
             if (2 * lane < valid) {
                 dg[at] = __float2bfloat16_rn(run);
-                dbg[at] = __float2bfloat16_rn(rvv[2 * lane] + db[0]);
+                dbeta[at] = __float2bfloat16_rn(db[0]);
             }
             if (2 * lane + 1 < valid) {
                 dg[at + p.nheads] = __float2bfloat16_rn(dc[1] + after);
-                dbg[at + p.nheads] = __float2bfloat16_rn(rvv[2 * lane + 1] + db[1]);
+                dbeta[at + p.nheads] = __float2bfloat16_rn(db[1]);
             }
         }
-    }
-    // dq, dk through the tiles of q and k to memory (rows past L are clipped)
+    } else {
+        const int q = w & 3, half = w >> 2;
+        const int t = 32 * q + lane, i = t & 63;             // TMEM lane: row of [k; q]; step of the chunk
+        const bool krows = q < 2;
+        const bool below = (q & 1) != 0 || half == 0;        // this warp's 32 x 32 of [ad; pd] reaches the triangle
+        const uint32_t lb = tmem + ((uint32_t)(q * 32) << 16);
+        const int c0 = HC * half;                            // this thread's columns of q and k
+        float2 acc[HC / 2];
 #pragma unroll
-    for (int n = 0; n < NTC; ++n) {
-        const uint32_t slab = ((nc0 + n) >> 3) * (C * 128) + 4 * tq;
-        const uint32_t o0 = slab + tile_off<128>(i0, (nc0 + n) & 7), o1 = slab + tile_off<128>(i0 + 8, (nc0 + n) & 7);
-        *reinterpret_cast<uint32_t*>(sm + L::Q + o0) = pack_bf16x2(dq[n][0], dq[n][1]);
-        *reinterpret_cast<uint32_t*>(sm + L::Q + o1) = pack_bf16x2(dq[n][2], dq[n][3]);
-        *reinterpret_cast<uint32_t*>(sm + L::K + o0) = pack_bf16x2(dk[n][0], dk[n][1]);
-        *reinterpret_cast<uint32_t*>(sm + L::K + o1) = pack_bf16x2(dk[n][2], dk[n][3]);
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
+        for (int e = 0; e < HC / 2; ++e) acc[e] = f2(0.0f, 0.0f);
+        bool ok = true;
+        for (int hh = 0; hh < hpg; ++hh) {
+            const double* cum = reinterpret_cast<const double*>(sm + L::CUM + (hh & 1) * L::CUM_BYTES);
+            const float* ef = reinterpret_cast<const float*>(cum + C);
+            const float* f = reinterpret_cast<const float*>(sm + L::F);
+            float* rowc = reinterpret_cast<float*>(sm + L::ROW + (hh & 1) * L::ROWS);
+            float* rowk = rowc + 4 * C;
+            float* rowb = rowk + 2 * C;
+            float* colv = rowb + 2 * C;
+            float* red = colv + 4 * C;
+            float rc = 0.0f, rk = 0.0f, rb = 0.0f;
+            if (!(ok = wwait(B_CUM + (hh & 1), hh >> 1) && wwait(B_RO, hh) && (hh == 0 || wwait(B_ACC, hh - 1)))) break;
+            const float eg = f[i], tail = f[C + i], beta = f[2 * C + i];
+            if (krows) {                                     // r.v over this thread's half of p
 #pragma unroll
-        for (int s = 0; s < DK / 64; ++s) {
-            tma_store_4d(&tm_dq, qs + s * C * 128, 64 * s, (int)grp, (int)t0, (int)b);
-            tma_store_4d(&tm_dk, ks + s * C * 128, 64 * s, (int)grp, (int)t0, (int)b);
+                for (int x = half * (DV / 16); x < (half + 1) * (DV / 16); ++x) {
+                    const uint4 vv = *reinterpret_cast<const uint4*>(sm + L::V + (x >> 3) * (SLAB / 2) + tile_off<128>(i, x & 7));
+                    const uint4 rr = *reinterpret_cast<const uint4*>(sm + L::RO + (x >> 3) * SLAB + tile_off<128>(i, x & 7));
+                    rb = fmaf(bf16_lo(vv.x), bf16_lo(rr.x), fmaf(bf16_hi(vv.x), bf16_hi(rr.x), rb));
+                    rb = fmaf(bf16_lo(vv.y), bf16_lo(rr.y), fmaf(bf16_hi(vv.y), bf16_hi(rr.y), rb));
+                    rb = fmaf(bf16_lo(vv.z), bf16_lo(rr.z), fmaf(bf16_hi(vv.z), bf16_hi(rr.z), rb));
+                    rb = fmaf(bf16_lo(vv.w), bf16_lo(rr.w), fmaf(bf16_hi(vv.w), bf16_hi(rr.w), rb));
+                }
+            }
+            if (!(ok = wwait(B_G, hh))) break;
+            tc_fence_after();
+            uint32_t ap[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ap[e] = 0u;
+            if (below) {
+                uint32_t g[32], kq[32];
+                tmem_ld32(lb + TG_G + 32 * half, g);
+                tmem_ld32(lb + TG_KQ + 32 * half, kq);
+                tmem_wait_ld();
+                // d: what multiplies r.u (minus the decay) or do.u (scale times it)
+                const float row = (krows ? -1.0f : p.scale) * ef[i];
+                const bool apart = wide[hh & 1] != 0;
+                float wv[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 fj = *reinterpret_cast<const float4*>(ef + C + 32 * half + e);
+                    float d[4] = {row * fj.x, row * fj.y, row * fj.z, row * fj.w};
+                    if (apart) {
+                        const float sgn = krows ? -1.0f : p.scale;
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = 32 * half + e + k;
+                            const float x = j <= i ? sgn * ex2_approx((float)((cum[i] - cum[j]) * kLog2e)) : 0.0f;
+                            d[0] = k == 0 ? x : d[0];
+                            d[1] = k == 1 ? x : d[1];
+                            d[2] = k == 2 ? x : d[2];
+                            d[3] = k == 3 ? x : d[3];
+                        }
+                    }
+                    float a[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = 32 * half + e + k;
+                        const float x = (krows ? j < i : j <= i) ? d[k] * __uint_as_float(g[e + k]) : 0.0f;
+                        const float s = __uint_as_float(kq[e + k]);
+                        if (krows) rb = fmaf(x, s, rb);
+                        a[k] = krows ? beta * x : x;
+                        wv[e + k] = j < i ? a[k] * s : 0.0f;
+                        rc += wv[e + k];
+                    }
+                    ap[e / 2] = pack_bf16x2(a[0], a[1]);
+                    ap[e / 2 + 1] = pack_bf16x2(a[2], a[3]);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 4 * half + c)) = make_uint4(ap[4 * c], ap[4 * c + 1], ap[4 * c + 2], ap[4 * c + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                arrive(B_AP);
+                float col[1];
+                butterfly_sum<32, 32>(wv, col, lane);        // lane j: the sum of column j over the warp's rows
+                colv[q * C + 32 * half + lane] = col[0];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 4 * half + c)) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                arrive(B_AP);
+            }
+            // <S, dS'>: both tiles have the same layout
+            if (!(ok = wwait(B_ST, hh))) break;
+            float sd = 0.0f;
+#pragma unroll 4
+            for (int x = tid; x < DV * DK / 8; x += 32 * GEPI) {
+                const uint4 a = *reinterpret_cast<const uint4*>(sm + L::S + x * 16), d = *reinterpret_cast<const uint4*>(sm + L::DS + x * 16);
+                sd = fmaf(bf16_lo(a.x), bf16_lo(d.x), fmaf(bf16_hi(a.x), bf16_hi(d.x), sd));
+                sd = fmaf(bf16_lo(a.y), bf16_lo(d.y), fmaf(bf16_hi(a.y), bf16_hi(d.y), sd));
+                sd = fmaf(bf16_lo(a.z), bf16_lo(d.z), fmaf(bf16_hi(a.z), bf16_hi(d.z), sd));
+                sd = fmaf(bf16_lo(a.w), bf16_lo(d.w), fmaf(bf16_hi(a.w), bf16_hi(d.w), sd));
+            }
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
+            if (lane == 0) red[w] = sd;
+            if (tid == 0) red[GEPI] = f[C - 1];
+            // Y and Z, 32 columns at a time
+            if (!(ok = wwait(B_YZ, hh))) break;
+            tc_fence_after();
+            float dy = 0.0f, dz = 0.0f;
+            const float fy = krows ? -beta * eg : p.scale * eg;
+#pragma unroll
+            for (int cc = 0; cc < HC / 32; ++cc) {
+                const int col = c0 + 32 * cc;
+                uint32_t y[32], z[32];
+                tmem_ld32(lb + TG_Y + col, y);
+                if (krows) tmem_ld32(lb + TG_Z + col, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 row = *reinterpret_cast<const uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c));
+                    const uint32_t r4[4] = {row.x, row.y, row.z, row.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int k = 8 * c + 2 * e;
+                        const float2 yy = f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+                        const float2 kk = f2(bf16_lo(r4[e]), bf16_hi(r4[e]));
+                        float2& a = acc[16 * cc + k / 2];
+                        a = fma2(f2(fy, fy), yy, a);
+                        dy = fmaf(yy.x, kk.x, fmaf(yy.y, kk.y, dy));
+                        if (krows) {
+                            const float2 zz = f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1]));
+                            a = fma2(f2(tail, tail), zz, a);
+                            dz = fmaf(zz.x, kk.x, fmaf(zz.y, kk.y, dz));
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            arrive(B_FREE);
+            rc = fmaf(fy, dy, rc);
+            if (krows) {
+                rk = tail * dz;
+                rb = fmaf(-eg, dy, rb);
+                rowk[half * C + i] = rk;
+                rowb[half * C + i] = rb;
+            }
+            rowc[half * 2 * C + t] = rc;
+            arrive(B_ROWS + (hh & 1));
         }
-        bulk_commit_group();
-        bulk_wait_all();                      // complete before the CTA exits
+        // dk, dq into the tile of k and q
+        if (ok && wwait(B_ACC, hpg - 1)) {
+            tc_fence_after();
+#pragma unroll
+            for (int cc = 0; cc < HC / 32; ++cc) {
+                const int col = c0 + 32 * cc;
+                uint32_t y[32];
+                tmem_ld32(lb + TG_ACC + col, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int k = 8 * c + 2 * e;
+                        const float2 a = add2(acc[16 * cc + k / 2], f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
+                        o[e] = pack_bf16x2(a.x, a.y);
+                    }
+                    *reinterpret_cast<uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            arrive(B_DONE);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (w == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -440,16 +463,16 @@ unsigned int read_and_clear_grad_error() {
 template <int DK, int DV>
 cudaError_t launch_grad(const GDRArgs& a, cudaStream_t s) {
     constexpr int bytes = GradSmem<DK, DV>::BYTES;
-    static_assert(bytes <= 227 * 1024, "shared memory");
-    CUtensorMap mk, mq, mdo, mdk, mdq;
+    CUtensorMap mk, mq, mv, mdo, mdk, mdq;
     cudaError_t e;
     if ((e = map_steps(&mk, a.k, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mq, a.q, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mdk, a.dk, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mdq, a.dq, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
+    if ((e = map_steps(&mv, a.v, DV, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mdo, a.dout, DV, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(gdr_bwd_grad_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    gdr_bwd_grad_kernel<DK, DV><<<(unsigned)(a.batch * a.ngroups * a.nchunks), 512, bytes, s>>>(mk, mq, mdo, mdk, mdq, a);
+    gdr_bwd_grad_kernel<DK, DV><<<(unsigned)(a.batch * a.ngroups * a.nchunks), GTHREADS, bytes, s>>>(mk, mq, mv, mdo, mdk, mdq, a);
     return cudaGetLastError();
 }
 
