@@ -59,21 +59,24 @@ namespace {
 // tiles and all of TMEM at P = N = 128).
 constexpr int SLAB = 128 * 128;                        // 64 columns of a stacked tile
 constexpr int GEPI = 8, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
-enum { B_QK = 0, B_RO = 1, B_ST = 2, B_G = 3, B_YZ = 4, B_AP = 5, B_ACC = 6, B_FREE = 7, B_CUM = 8, B_ROWS = 10, B_DONE = 12, NGBAR = 13 };   // B_CUM, B_ROWS: by head parity
+// (B_CUM, B_ROWS: by head parity; B_RO, B_ST, B_FREE: by slot)
+enum { B_QK = 0, B_G = 1, B_YZ = 2, B_YZF = 3, B_AP = 4, B_ACC = 5, B_DONE = 6, B_CUM = 7, B_ROWS = 9, B_RO = 11, B_ST = 13, B_FREE = 15, NGBAR = 17 };
 
 template <int DK, int DV>
 struct GradSmem {
-    static constexpr int KQ = 0, RO = KQ + DK / 64 * SLAB, U = RO + DV / 64 * SLAB, S = U + DV / 64 * (SLAB / 2);
-    static constexpr int DS = S + DV * DK * 2, V = DS + DV * DK * 2, AP = V + DV / 64 * (SLAB / 2), Z0 = AP + SLAB;
-    static constexpr int F = Z0 + SLAB;                // eg, tail, beta
+    static constexpr int KQ = 0, AP = DK / 64 * SLAB, Z0 = AP + SLAB, SLOTS0 = Z0 + SLAB;
+    // a slot: the tiles of one head; two of them where they fit, so that the next head's loads run ahead
+    static constexpr int RO = 0, U = DV / 64 * SLAB, S = U + DV / 64 * (SLAB / 2), DS = S + DV * DK * 2, V = DS + DV * DK * 2;
+    static constexpr int F = V + DV / 64 * (SLAB / 2), SLOT = F + 1024;    // F: eg, tail, beta
+    static constexpr int NS = DV == 64 ? 2 : 1;
     // by head parity: the decays (double c[C], float e^(c - mid), e^(mid - c), [C]) ...
-    static constexpr int CUM = F + 3 * C * 4, CUM_BYTES = C * 8 + 2 * C * 4;
+    static constexpr int CUM = SLOTS0 + NS * SLOT, CUM_BYTES = C * 8 + 2 * C * 4;
     // ... and the sums: by column half, of dc by row of [k; q], of e^.. k.(dS' u) and of dbeta by row of k;
     // the column sums by lane quarter; <S, dS'> by warp
     static constexpr int ROW = CUM + 2 * CUM_BYTES, ROWS = 2 * 4 * C * 4 + 4 * C * 4 + 64;
     static constexpr int WIDE = ROW + 2 * ROWS, BAR = WIDE + 16, TSLOT = BAR + NGBAR * 8, ABORT = TSLOT + 8;
     static constexpr int BYTES = ABORT + 8 + 1024;
-    static_assert(BYTES <= 227 * 1024 && U % 1024 == 0 && S % 1024 == 0 && AP % 1024 == 0, "shared memory");
+    static_assert(BYTES <= 227 * 1024 && U % 1024 == 0 && S % 1024 == 0 && SLOT % 1024 == 0, "shared memory");
 };
 constexpr uint32_t TG_KQ = 0, TG_G = 64, TG_ACC = 128, TG_Y = 256, TG_Z = 384;
 
@@ -98,7 +101,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int* wide = reinterpret_cast<int*>(sm + L::WIDE);
     auto bar = [&](int i) { return base + L::BAR + 8u * (uint32_t)i; };
     if (tid == 0) {
-        const int counts[NGBAR] = {1, 1, 1, 1, 1, GEPI, 1, GEPI + 1, 1, 1, GEPI, GEPI, GEPI};
+        const int counts[NGBAR] = {1, 1, 1, GEPI, GEPI, 1, GEPI, 1, 1, GEPI, GEPI, 1, 1, 1, 1, GEPI + 1, GEPI + 1};
         for (int i = 0; i < NGBAR; ++i) mbar_init(bar(i), counts[i]);
         *abort_flag = 0;
         fence_barrier_init();
@@ -128,7 +131,9 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (lane == 0) {
             bool live = true;
             for (int hh = 0; hh < hpg && !p.stall; ++hh) {   // (stall: test only, nothing staged, every wait runs out)
-                if (hh > 0 && !(live = wait(B_FREE, hh - 1))) break;
+                const int sl = hh % L::NS;
+                if (hh >= L::NS && !(live = wait(B_FREE + sl, hh / L::NS - 1))) break;
+                const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = bar(B_RO + sl), st = bar(B_ST + sl);
                 const int h = h0 + hh;
                 const int64_t rec = (b * p.nheads + h) * p.nchunks + ch;
                 if (hh == 0) {
@@ -139,18 +144,18 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         tma_load_4d(base + L::KQ + s * SLAB + SLAB / 2, &tm_q, bar(B_QK), 64 * s, (int)grp, (int)t0, (int)b);
                     }
                 }
-                mbar_expect_tx(bar(B_RO), TV * 2 * SLAB + 3 * C * 4);
+                mbar_expect_tx(ro, TV * 2 * SLAB + 3 * C * 4);
 #pragma unroll
                 for (int t = 0; t < TV; ++t) {
-                    bulk_load(base + L::RO + t * SLAB, static_cast<const unsigned char*>(p.dr) + (rec * TV + t) * (SLAB / 2), SLAB / 2, bar(B_RO));
-                    tma_load_4d(base + L::RO + t * SLAB + SLAB / 2, &tm_do, bar(B_RO), 64 * t, h, (int)t0, (int)b);
-                    tma_load_4d(base + L::V + t * (SLAB / 2), &tm_v, bar(B_RO), 64 * t, h, (int)t0, (int)b);
+                    bulk_load(slot + L::RO + t * SLAB, static_cast<const unsigned char*>(p.dr) + (rec * TV + t) * (SLAB / 2), SLAB / 2, ro);
+                    tma_load_4d(slot + L::RO + t * SLAB + SLAB / 2, &tm_do, ro, 64 * t, h, (int)t0, (int)b);
+                    tma_load_4d(slot + L::V + t * (SLAB / 2), &tm_v, ro, 64 * t, h, (int)t0, (int)b);
                 }
-                bulk_load(base + L::U, static_cast<const unsigned char*>(p.u) + rec * TV * (SLAB / 2), TV * (SLAB / 2), bar(B_RO));
-                bulk_load(base + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, bar(B_RO));
-                mbar_expect_tx(bar(B_ST), 2 * DV * DK * 2);
-                bulk_load(base + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * DK * 2, DV * DK * 2, bar(B_ST));
-                bulk_load(base + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * DK * 2, DV * DK * 2, bar(B_ST));
+                bulk_load(slot + L::U, static_cast<const unsigned char*>(p.u) + rec * TV * (SLAB / 2), TV * (SLAB / 2), ro);
+                bulk_load(slot + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, ro);
+                mbar_expect_tx(st, 2 * DV * DK * 2);
+                bulk_load(slot + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * DK * 2, DV * DK * 2, st);
+                bulk_load(slot + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * DK * 2, DV * DK * 2, st);
             }
             // dq, dk, staged in the tile of k and q (rows past L are clipped)
             if (live && wait(B_DONE, 0)) {
@@ -164,7 +169,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             bulk_wait_all();                                 // complete before the CTA exits
         }
     } else if (w == G_MMA) {
-        const uint32_t kq = base + L::KQ, ro = base + L::RO, u = base + L::U, ap = base + L::AP;
+        const uint32_t kq = base + L::KQ, ap = base + L::AP;
         constexpr uint32_t ID64 = umma_idesc_bf16(128, 64, 0, 0), IDKK = umma_idesc_bf16(128, DK, 0, 0),
                            IDKN = umma_idesc_bf16(128, DK, 0, 1), IDNN = umma_idesc_bf16(128, DK, 1, 1);
         auto kmaj = [&](uint32_t tile, int s, uint32_t stride) { return umma_desc_sw128(tile + (s >> 2) * stride + (s & 3) * 32, 16, 1024); };
@@ -175,17 +180,21 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int s = 0; s < DK / 16; ++s) umma_elect(tmem + TG_KQ, kmaj(kq, s, SLAB), kmaj(kq, s, SLAB), ID64, s > 0);
         }
         for (int hh = 0; hh < hpg && live; ++hh) {
-            if (!(live = wwait(B_RO, hh))) break;
+            const int sl = hh % L::NS;
+            const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = slot + L::RO, u = slot + L::U;
+            if (!(live = wwait(B_RO + sl, hh / L::NS))) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_G, kmaj(ro, s, SLAB), kmaj(u, s, SLAB / 2), ID64, s > 0);
             commit_elect(bar(B_G));
-            if (!(live = wwait(B_ST, hh))) break;
+            if (!(live = wwait(B_ST + sl, hh / L::NS) && (hh == 0 || wwait(B_YZF, hh - 1)))) break;
+            tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Y, kmaj(ro, s, SLAB), kmaj(base + L::S, s, DK * 128), IDKK, s > 0);
+            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Y, kmaj(ro, s, SLAB), kmaj(slot + L::S, s, DK * 128), IDKK, s > 0);
 #pragma unroll
-            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Z, kmaj(u, s, SLAB / 2), kmaj(base + L::DS, s, DK * 128), IDKK, s > 0);
+            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Z, kmaj(u, s, SLAB / 2), kmaj(slot + L::DS, s, DK * 128), IDKK, s > 0);
             commit_elect(bar(B_YZ));
+            commit_elect(bar(B_FREE + sl));
             if (!(live = wwait(B_AP, hh))) break;
             tc_fence_after();
 #pragma unroll
@@ -195,7 +204,6 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int s = 0; s < 2 * C / 16; ++s)
                 umma_elect(tmem + TG_ACC, umma_desc_sw128(ap + s * 2048, L::Z0 - L::AP, 1024), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDNN, 1u);
             commit_elect(bar(B_ACC));
-            commit_elect(bar(B_FREE));
         }
         if (live) wwait(B_ACC, hpg - 1);                     // the last commit must land before the CTA may exit
     } else if (w == G_AUX) {
@@ -279,20 +287,22 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int hh = 0; hh < hpg; ++hh) {
             const double* cum = reinterpret_cast<const double*>(sm + L::CUM + (hh & 1) * L::CUM_BYTES);
             const float* ef = reinterpret_cast<const float*>(cum + C);
-            const float* f = reinterpret_cast<const float*>(sm + L::F);
+            const int sl = hh % L::NS;
+            const unsigned char* slot = sm + L::SLOTS0 + sl * L::SLOT;
+            const float* f = reinterpret_cast<const float*>(slot + L::F);
             float* rowc = reinterpret_cast<float*>(sm + L::ROW + (hh & 1) * L::ROWS);
             float* rowk = rowc + 4 * C;
             float* rowb = rowk + 2 * C;
             float* colv = rowb + 2 * C;
             float* red = colv + 4 * C;
             float rc = 0.0f, rk = 0.0f, rb = 0.0f;
-            if (!(ok = wwait(B_CUM + (hh & 1), hh >> 1) && wwait(B_RO, hh) && (hh == 0 || wwait(B_ACC, hh - 1)))) break;
+            if (!(ok = wwait(B_CUM + (hh & 1), hh >> 1) && wwait(B_RO + sl, hh / L::NS) && (hh == 0 || wwait(B_ACC, hh - 1)))) break;
             const float eg = f[i], tail = f[C + i], beta = f[2 * C + i];
             if (krows) {                                     // r.v over this thread's half of p
 #pragma unroll
                 for (int x = half * (DV / 16); x < (half + 1) * (DV / 16); ++x) {
-                    const uint4 vv = *reinterpret_cast<const uint4*>(sm + L::V + (x >> 3) * (SLAB / 2) + tile_off<128>(i, x & 7));
-                    const uint4 rr = *reinterpret_cast<const uint4*>(sm + L::RO + (x >> 3) * SLAB + tile_off<128>(i, x & 7));
+                    const uint4 vv = *reinterpret_cast<const uint4*>(slot + L::V + (x >> 3) * (SLAB / 2) + tile_off<128>(i, x & 7));
+                    const uint4 rr = *reinterpret_cast<const uint4*>(slot + L::RO + (x >> 3) * SLAB + tile_off<128>(i, x & 7));
                     rb = fmaf(bf16_lo(vv.x), bf16_lo(rr.x), fmaf(bf16_hi(vv.x), bf16_hi(rr.x), rb));
                     rb = fmaf(bf16_lo(vv.y), bf16_lo(rr.y), fmaf(bf16_hi(vv.y), bf16_hi(rr.y), rb));
                     rb = fmaf(bf16_lo(vv.z), bf16_lo(rr.z), fmaf(bf16_hi(vv.z), bf16_hi(rr.z), rb));
@@ -359,11 +369,11 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 arrive(B_AP);
             }
             // <S, dS'>: both tiles have the same layout
-            if (!(ok = wwait(B_ST, hh))) break;
+            if (!(ok = wwait(B_ST + sl, hh / L::NS))) break;
             float sd = 0.0f;
 #pragma unroll 4
             for (int x = tid; x < DV * DK / 8; x += 32 * GEPI) {
-                const uint4 a = *reinterpret_cast<const uint4*>(sm + L::S + x * 16), d = *reinterpret_cast<const uint4*>(sm + L::DS + x * 16);
+                const uint4 a = *reinterpret_cast<const uint4*>(slot + L::S + x * 16), d = *reinterpret_cast<const uint4*>(slot + L::DS + x * 16);
                 sd = fmaf(bf16_lo(a.x), bf16_lo(d.x), fmaf(bf16_hi(a.x), bf16_hi(d.x), sd));
                 sd = fmaf(bf16_lo(a.y), bf16_lo(d.y), fmaf(bf16_hi(a.y), bf16_hi(d.y), sd));
                 sd = fmaf(bf16_lo(a.z), bf16_lo(d.z), fmaf(bf16_hi(a.z), bf16_hi(d.z), sd));
@@ -373,6 +383,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int m = 16; m >= 1; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
             if (lane == 0) red[w] = sd;
             if (tid == 0) red[GEPI] = f[C - 1];
+            arrive(B_FREE + sl);
             // Y and Z, 32 columns at a time
             if (!(ok = wwait(B_YZ, hh))) break;
             tc_fence_after();
@@ -406,7 +417,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
             }
             tc_fence_before();
-            arrive(B_FREE);
+            arrive(B_YZF);
             rc = fmaf(fy, dy, rc);
             if (krows) {
                 rk = tail * dz;
