@@ -14,11 +14,16 @@
 // cancellation when the mean is large) and the output take one read of
 // memory.  All statistics and sums are fp32.
 //
-// The forward gives each group of TPR threads one row (16 elements a thread)
-// and lets many small blocks overlap.  The backward keeps 8 elements a thread
-// and as many blocks as the SMs hold; they walk the rows in a grid-stride loop
-// with the next row's loads issued before this row's sums, the weights and
-// the sums of a thread's columns in registers over all its rows.
+// Both directions run as many blocks as the SMs hold, which walk the rows in a
+// grid-stride loop, the weights and (backward) the sums of a thread's columns in
+// registers over all its rows.  The next rows are on their way to shared memory
+// meanwhile: HBM's latency times its rate is 40 KB an SM in flight, more than
+// the registers have room for beside the row at work.  Measured against the
+// copy engine (44 us for the forward's 268 MB at 32768 rows of 2048, bf16):
+// forward 50 us, backward (402 MB) 72; with a row a block and no loop 61, with
+// the next row in registers 89.  Rows of more than 4096 columns or of no whole
+// number of 16-byte pieces, and calls of so few rows that no block has two,
+// take a row a block in the forward; the backward prefetches to registers.
 //
 // The weight's gradient: every block writes one partial row to the workspace,
 // and a second kernel adds the partials in block order: no atomics, so the
@@ -31,7 +36,6 @@
 namespace mmscan {
 
 namespace {
-
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.0f, 1.0f + ex2_approx(-z * kLog2e)); }
 
@@ -115,6 +119,113 @@ struct Raw {
     __device__ __forceinline__ void get(float* f) const { load_vec<IO, VEC>(reinterpret_cast<const IO*>(&v), f); }
 };
 
+// Rows on their way: every thread copies its own pieces of 16 bytes of the next
+// rows to slots of its own in shared memory (cp.async) and reads nobody else's,
+// so that a wait for its own copies is all it takes, and what is in flight
+// costs no registers.
+// Rows in flight, this one's included: four (six or eight measured the same or
+// slower, the L1 being smaller), as far as the SM's shared memory goes.
+constexpr int ring_depth(int stage, int blocks) {
+    const int d = 200 * 1024 / (stage * blocks);
+    return d > 4 ? 4 : d < 2 ? 2 : d;
+}
+constexpr bool norm_ring(int vec, int tpr) { return vec > 1 && tpr <= 256; }
+
+constexpr int norm_fwd_resident(int bt, int elems) { return (elems > 8 ? 768 : 1024) / bt; }
+template <int BT, int NV, int VEC, bool GATE>
+struct FwdRing {
+    static constexpr int STAGE = BT * NV * 16 * (GATE ? 2 : 1), D = ring_depth(STAGE, norm_fwd_resident(BT, NV * VEC));
+};
+
+template <typename IO, int VEC, int TPR, int NV, bool GATE>
+__global__ void __launch_bounds__(norm_block(TPR), norm_fwd_resident(norm_block(TPR), NV * VEC)) norm_fwd_ring_kernel(const NormArgs p) {
+    constexpr int BT = norm_block(TPR), RPB = BT / TPR;
+    constexpr int STAGE = FwdRing<BT, NV, VEC, GATE>::STAGE, D = FwdRing<BT, NV, VEC, GATE>::D;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
+    int slot = 0;
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const int cols = (int)p.cols;
+    unsigned char* const own = ring + threadIdx.x * 16;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    auto fetch = [&](int64_t r0, int stage) {
+        if (r0 < p.rows) {
+            const int64_t base = (r0 + grp < p.rows ? r0 + grp : p.rows - 1) * cols;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t + i * TPR) * VEC;
+                if (c >= cols) continue;
+                cp_async_16(own + stage * STAGE + i * BT * 16, static_cast<const IO*>(p.x) + base + c, 16);
+                if constexpr (GATE) cp_async_16(own + stage * STAGE + (NV + i) * BT * 16, static_cast<const IO*>(p.z) + base + c, 16);
+            }
+        }
+        cp_async_commit();
+    };
+    int64_t r0 = (int64_t)blockIdx.x * RPB;
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) fetch(r0 + d * step, d);
+    float w[NV * VEC], b[NV * VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * TPR) * VEC;
+        load_param<VEC>(p.weight && c < cols ? p.weight + c : nullptr, w + i * VEC, 1.0f);
+        load_param<VEC>(p.bias && c < cols ? p.bias + c : nullptr, b + i * VEC, 0.0f);
+    }
+    for (int now = 0; r0 < p.rows; r0 += step, now = now + 1 == D ? 0 : now + 1) {
+        cp_async_wait<D - 2>();
+        const unsigned char* mine = own + now * STAGE;
+        float v[NV * VEC];
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[i * VEC + e] = 0.0f;
+            if ((t + i * TPR) * VEC < cols) load_vec<IO, VEC>(reinterpret_cast<const IO*>(mine + i * BT * 16), v + i * VEC);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s.x += v[i * VEC + e];
+        }
+        float mean = 0.0f;
+        if (!p.rms) mean = row_sum<TPR>(s, red, slot).x * p.inv_cols;
+        s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = (t + i * TPR) * VEC < cols;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                v[i * VEC + e] -= mean;
+                if (in) s.x = fmaf(v[i * VEC + e], v[i * VEC + e], s.x);
+            }
+        }
+        const float var = row_sum<TPR>(s, red, slot).x * p.inv_cols;
+        const float rstd = 1.0f / sqrtf(var + p.eps);
+        const int64_t row = r0 + grp;
+        if (row < p.rows) {
+            if (t == 0) {
+                if (p.mean && !p.rms) p.mean[row] = mean;
+                if (p.rstd) p.rstd[row] = rstd;
+            }
+            IO* y = static_cast<IO*>(p.y) + row * cols;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t + i * TPR) * VEC;
+                if (c >= cols) continue;
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i * VEC + e] * rstd, w[i * VEC + e], b[i * VEC + e]);
+                if constexpr (GATE) {
+                    float z[VEC];
+                    load_vec<IO, VEC>(reinterpret_cast<const IO*>(mine + (NV + i) * BT * 16), z);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] *= z[e] * sigmoid_f32(z[e]);
+                }
+                store_vec<IO, VEC>(y + c, o);
+            }
+        }
+        // into the slots of the row before this one
+        fetch(r0 + (D - 1) * step, now == 0 ? D - 1 : now - 1);
+    }
+}
+
 template <typename IO, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArgs p) {
     constexpr int RPB = norm_block(TPR) / TPR;
@@ -180,12 +291,27 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArg
 // Resident blocks an SM that the backward's grid counts on: 24 warps at 8
 // elements a thread in 16-byte pieces (up to 80 registers); 16 by element or
 // at 16 elements (128 registers; a block of 1024 threads has 64 and spills).
+// (28 and 20 warps spill or crowd the ring: 62 and 92 us against 56 and 72.)
 constexpr int norm_bwd_resident(int bt, int elems, int vec) { return bt >= 512 ? 1 : elems > 8 || vec == 1 ? 512 / bt : 768 / bt; }
+
+// A thread's slots of a row: x, dy (z); then the row's mean and rstd, in rows of
+// a warp and more once a warp (all its lanes copying one address take turns: 136
+// us against 87, 32768 rows of 2048), in narrower ones for every thread (56 us
+// against 58, 524288 gated rows of 64).
+template <int BT, int TPR, int NV, int VEC, bool GATE>
+struct BwdRing {
+    static constexpr int LANES = TPR < 32 ? 1 : 32;
+    static constexpr int STATS = BT * NV * 16 * (GATE ? 3 : 2), STAGE = STATS + BT / LANES * 8;
+    static constexpr int D = ring_depth(STAGE, norm_bwd_resident(BT, NV * VEC, VEC));
+};
 
 template <typename IO, int VEC, int TPR, int NV, bool GATE>
 __global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(TPR), NV * VEC, VEC)) norm_bwd_kernel(const NormArgs p) {
     constexpr int BT = norm_block(TPR);
     constexpr int RPB = BT / TPR;
+    constexpr bool RING = norm_ring(VEC, TPR);
+    using R = BwdRing<BT, TPR, NV, VEC, GATE>;
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
     int slot = 0;
     const int t = threadIdx.x % TPR;
@@ -217,11 +343,53 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(
             if constexpr (GATE) rz[i].load(static_cast<const IO*>(p.z) + base + c);
         }
     };
+    unsigned char* const own = ring + threadIdx.x * 16;
+    unsigned char* const stats = ring + R::STATS + threadIdx.x / R::LANES * 8;
+    auto copy = [&](int64_t r0, int stage) {
+        if (r0 < p.rows) {
+            const int64_t row = r0 + grp < p.rows ? r0 + grp : p.rows - 1, base = row * cols;
+            if (threadIdx.x % R::LANES == 0) {
+                if (!p.rms) cp_async_4(stats + stage * R::STAGE, p.mean + row, 4);
+                cp_async_4(stats + stage * R::STAGE + 4, p.rstd + row, 4);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t + i * TPR) * VEC;
+                if (c >= cols) continue;
+                unsigned char* const at = own + stage * R::STAGE + i * BT * 16;
+                cp_async_16(at, static_cast<const IO*>(p.x) + base + c, 16);
+                cp_async_16(at + NV * BT * 16, static_cast<const IO*>(p.dy) + base + c, 16);
+                if constexpr (GATE) cp_async_16(at + 2 * NV * BT * 16, static_cast<const IO*>(p.z) + base + c, 16);
+            }
+        }
+        cp_async_commit();
+    };
     int64_t r0 = (int64_t)blockIdx.x * RPB;
-    constexpr bool kAhead = VEC > 1 || (NV <= 8 && TPR < 1024);   // elements one by one: as registers allow
-    if (kAhead) fetch(r0);
+    constexpr bool kAhead = !RING && (VEC > 1 || (NV <= 8 && TPR < 1024));   // elements one by one: as registers allow
+    int now = 0;
+    if constexpr (RING) {
+#pragma unroll
+        for (int d = 0; d < R::D - 1; ++d) copy(r0 + d * step, d);
+    } else if constexpr (kAhead) {
+        fetch(r0);
+    }
     for (; r0 < p.rows; r0 += step) {
-        if (!kAhead) fetch(r0);
+        if constexpr (RING) {
+            cp_async_wait<R::D - 2>();
+            __syncwarp();                                    // the statistics are another lane's copy
+            const unsigned char* mine = own + now * R::STAGE;
+            const float2 st = *reinterpret_cast<const float2*>(stats + now * R::STAGE);
+            mean = p.rms ? 0.0f : st.x;
+            rstd = st.y;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                rx[i].load(reinterpret_cast<const IO*>(mine + i * BT * 16));
+                ry[i].load(reinterpret_cast<const IO*>(mine + (NV + i) * BT * 16));
+                if constexpr (GATE) rz[i].load(reinterpret_cast<const IO*>(mine + (2 * NV + i) * BT * 16));
+            }
+        } else if constexpr (!kAhead) {
+            fetch(r0);
+        }
         const bool active = r0 + grp < p.rows;
         const int64_t base = (r0 + grp) * cols;
         const float rs = rstd;
@@ -263,7 +431,12 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_bwd_resident(norm_block(
                 s.y = fmaf(d[k], xh[k], s.y);
             }
         }
-        if (kAhead && r0 + step < p.rows) fetch(r0 + step);
+        if constexpr (RING) {                                // into the slots of the row before this one
+            copy(r0 + (R::D - 1) * step, now == 0 ? R::D - 1 : now - 1);
+            now = now + 1 == R::D ? 0 : now + 1;
+        } else if constexpr (kAhead) {
+            if (r0 + step < p.rows) fetch(r0 + step);
+        }
         s = row_sum<TPR>(s, red, slot);
         const float a0 = p.rms ? 0.0f : s.x * p.inv_cols;
         const float a1 = s.y * p.inv_cols;
@@ -353,10 +526,37 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float* part, int
     }
 }
 
+// The attribute is needed past 48 KB only.
+template <typename Kernel>
+cudaError_t launch_ring(Kernel kernel, int blocks, int bt, int bytes, const NormArgs& a, cudaStream_t s) {
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<blocks, bt, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename IO, int VEC, int TPR, int NV, bool GATE>
+cudaError_t launch_fwd_ring(const NormArgs& a, int blocks, cudaStream_t s) {
+    using R = FwdRing<norm_block(TPR), NV, VEC, GATE>;
+    return launch_ring(norm_fwd_ring_kernel<IO, VEC, TPR, NV, GATE>, blocks, norm_block(TPR), R::D * R::STAGE, a, s);
+}
+
+template <typename IO, int VEC, int TPR, int NV, bool GATE>
+cudaError_t launch_bwd_rows(const NormArgs& a, int blocks, cudaStream_t s) {
+    using R = BwdRing<norm_block(TPR), TPR, NV, VEC, GATE>;
+    return launch_ring(norm_bwd_kernel<IO, VEC, TPR, NV, GATE>, blocks, norm_block(TPR), norm_ring(VEC, TPR) ? R::D * R::STAGE : 0, a, s);
+}
+
 template <typename IO, int VEC, int TPR, int NV>
 cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
     constexpr int BT = norm_block(TPR), RPB = BT / TPR;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
+    if constexpr (norm_ring(VEC, TPR)) {                     // where blocks have several rows each
+        constexpr int resident = norm_fwd_resident(BT, NV * VEC);
+        if (blocks > 148 * resident) return a.z ? launch_fwd_ring<IO, VEC, TPR, NV, true>(a, 148 * resident, s) : launch_fwd_ring<IO, VEC, TPR, NV, false>(a, 148 * resident, s);
+    }
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     norm_fwd_kernel<IO, VEC, TPR, NV><<<(unsigned)blocks, BT, 0, s>>>(a);
     return cudaGetLastError();
@@ -365,17 +565,14 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
 template <typename IO, int VEC, int TPR, int NV>
 cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s) {
     const int blocks = norm_bwd_blocks(a.rows, a.cols, sizeof(IO) == 4 ? 0 : 1);
-    if (a.z) norm_bwd_kernel<IO, VEC, TPR, NV, true><<<blocks, norm_block(TPR), 0, s>>>(a);
-    else norm_bwd_kernel<IO, VEC, TPR, NV, false><<<blocks, norm_block(TPR), 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = a.z ? launch_bwd_rows<IO, VEC, TPR, NV, true>(a, blocks, s) : launch_bwd_rows<IO, VEC, TPR, NV, false>(a, blocks, s);
     if (e != cudaSuccess || !a.part) return e;
     norm_param_kernel<<<(unsigned)((2 * a.cols + 31) / 32), dim3(32, 32), 0, s>>>(a.part, blocks, a.cols, a.dweight, a.dbias);
     return cudaGetLastError();
 }
 
-// Forward: threads of a row at 16 elements each (8 in rows of up to 256).
-// Measured (33.5 M elements in rows of 2048, bf16): 61 us at 16 elements, 81 at
-// 8, 65 at 64 (a warp a row); 84 for a grid that stays and walks the rows.
+// Forward: threads of a row at 16 elements each (8 in rows of up to 256; a row a
+// block, 32768 rows of 2048 in bf16: 61 us at 16, 81 at 8, 65 at 64).
 template <typename IO, int VEC>
 cudaError_t launch_fwd_vec(const NormArgs& a, cudaStream_t s) {
     if (a.cols <= 8) return launch_fwd<IO, VEC, 1, 8 / VEC>(a, s);
@@ -394,15 +591,16 @@ cudaError_t launch_fwd_vec(const NormArgs& a, cudaStream_t s) {
     return launch_fwd<IO, VEC, 1024, 16 / VEC>(a, s);
 }
 
-// Backward: threads of a row at 8 elements each; at 16 past 2048 columns in
-// 16-byte pieces, past 8192 by element.
+// Backward: threads of a row at 8 elements each; at 16 past 1024 columns in
+// 16-byte pieces (72 us against 87, 32768 rows of 2048 in bf16: fewer warps take
+// part in a row's sums), past 8192 by element.
 int norm_bwd_tpr(int64_t cols, int vec) {
     if (cols <= 64) return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
-    if (cols <= 2048) return cols <= 256 ? 32 : cols <= 1024 ? 128 : 256;
+    if (cols <= 2048) return cols <= 256 ? 32 : cols <= 1024 || vec > 1 ? 128 : 256;
     if (vec == 1) return cols <= 4096 ? 512 : 1024;
     return cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
 }
-int norm_bwd_elems(int64_t cols, int vec) { return cols <= (vec == 1 ? 8192 : 2048) ? 8 : 16; }
+int norm_bwd_elems(int64_t cols, int vec) { return cols <= (vec == 1 ? 8192 : 1024) ? 8 : 16; }
 
 template <typename IO, int VEC>
 cudaError_t launch_bwd_vec(const NormArgs& a, cudaStream_t s) {
@@ -419,6 +617,8 @@ cudaError_t launch_bwd_vec(const NormArgs& a, cudaStream_t s) {
         case 128:
             if constexpr (VEC == 1)
                 if (a.cols <= 512) return launch_bwd<IO, 1, 128, 4>(a, s);
+            if constexpr (VEC > 1)
+                if (!eight) return launch_bwd<IO, VEC, 128, 16 / VEC>(a, s);
             return launch_bwd<IO, VEC, 128, 8 / VEC>(a, s);
         case 256:
             if (eight) return launch_bwd<IO, VEC, 256, 8 / VEC>(a, s);

@@ -90,6 +90,21 @@ def test_many_rows():
     _check(3001, 2048, torch.bfloat16, "wb", rms=False)
 
 
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("cols", [8, 16, 24, 64, 200, 512, 1000, 1536, 2048, 2056, 4096])
+def test_several_rows_a_block(cols, io):
+    """Every thread layout with several rows to a block, the last round of them not full; a
+    row's results are those of a call of a few rows."""
+    rows = 6_000_000 // cols | 1
+    _check(rows, cols, io, "wbz", rms=False)
+    _check(rows, cols, io, "wb", rms=True)
+    x, w, b, z, _ = _inputs(rows, cols, io, 5, True, True, True)
+    for gate in (None, z):
+        every = mm.layer_norm_fwd(x, w, b, z=gate)
+        few = mm.layer_norm_fwd(x[-7:], w, b, z=None if gate is None else gate[-7:])
+        assert all(torch.equal(m[-7:], f) for m, f in zip(every, few))
+
+
 def test_mean_far_from_zero_and_constant_rows():
     _check(9, 1024, torch.float32, "wb", rms=False, offset=3e3)
     _check(9, 1536, torch.bfloat16, "wb", rms=False, offset=50.0)
