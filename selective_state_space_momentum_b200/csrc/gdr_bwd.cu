@@ -24,7 +24,7 @@
 // forms the rest.  dq and dk of a group sum over its heads inside one block:
 // no atomics, the same bits in every run.
 //
-// Precision: every gradient leaves as bf16 (2^-9).  The operands of the
+// Precision: every gradient leaves as bf16 (2^-8).  The operands of the
 // products are rounded to bf16 once each; products, sums, dS, the row sums
 // and dc are fp32 or wider.  dh0 carries the products' operand rounding.
 #include <cuda.h>

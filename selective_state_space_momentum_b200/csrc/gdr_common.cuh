@@ -23,8 +23,8 @@ constexpr int REC_T = 0, REC_P = C * C * 2, REC_F = 2 * C * C * 2;
 constexpr int REC_BYTES = REC_F + 3 * C * 4;
 static_assert(REC_BYTES == kGdrRecBytes, "record size");
 
-// Tiles in shared memory: rows of 128 or 256 bytes, the 16-byte pieces of a
-// row permuted by the row's number mod 8, so that the eight rows an ldmatrix
+// Tiles in shared memory: rows of 128 bytes, the 16-byte pieces of a row
+// permuted by the row's number mod 8, so that the eight rows an ldmatrix
 // reads at one column lie in different banks.
 template <int RB>
 __device__ __forceinline__ uint32_t tile_off(int row, int c16) {
@@ -51,16 +51,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 
 // Operand fragments from a tile; `lane` 0..31, every index in elements of 8
 // (c16) or rows.
-// B (k x n) of two neighbouring n-tiles from a tile stored [n][k] / [k][n].
+// B (k x n) of two neighbouring n-tiles from a tile stored [n][k].
 template <int RB>
 __device__ __forceinline__ void load_b_nk(uint32_t tile, int n0, int kc, int lane, uint32_t (&r)[4]) {
     const int m = lane >> 3;
     ldsm4(tile + tile_off<RB>(n0 + (m >> 1) * 8 + (lane & 7), kc + (m & 1)), r);
-}
-template <int RB>
-__device__ __forceinline__ void load_b_kn(uint32_t tile, int k0, int nc, int lane, uint32_t (&r)[4]) {
-    const int m = lane >> 3;
-    ldsm4t(tile + tile_off<RB>(k0 + (m & 1) * 8 + (lane & 7), nc + (m >> 1)), r);
 }
 // A (16 x 16) from a tile stored [m][k] / [k][m].
 template <int RB>
@@ -74,7 +69,7 @@ __device__ __forceinline__ void load_a_km(uint32_t tile, int k0, int mc, int lan
     ldsm4t(tile + tile_off<RB>(k0 + (m >> 1) * 8 + (lane & 7), mc + (m & 1)), r);
 }
 
-// fp32 values in two bf16 terms: hi + lo is the fp32 value to 2^-17.
+// fp32 values in two bf16 terms: hi + lo is the fp32 value to 2^-16.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16x2(x, y);
     lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));

@@ -14,8 +14,8 @@
 // gdr_chain_kernel (gdr_chain.cu) walks the chunks in order.
 //
 // Precision: the state is fp32.  Where it enters a product it is split in two
-// bf16 terms (hi + lo, 2^-17), and so are v - e^c S k, T and e^c u; k, q, v are bf16
-// already.  The outputs o are rounded to bf16 anyway (2^-9), so the products
+// bf16 terms (hi + lo, 2^-16), and so are v - e^c S k, T and e^c u; k, q, v are bf16
+// already.  The outputs o are rounded to bf16 anyway (2^-8), so the products
 // that reach only o take the hi terms of u alone.
 #include <cuda.h>
 

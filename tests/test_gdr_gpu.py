@@ -279,3 +279,56 @@ def test_layer_forward_and_backward():
     row_tol = 4 * float(rows.square().mean().sqrt()) + 4 * BF16
     for name, t in grads.items():
         assert float((t.double() - want[name]).norm() / want[name].norm()) <= GRAD_TOL + row_tol, name
+
+
+def test_two_calls_at_once():
+    """Two streams, each its own call with its own workspace, many times over."""
+    sets = [plain.inputs(2, 200, 4, 2, 128, 64, seed=s, device="cuda", carry=True) for s in (11, 12)]
+    want = [mm.gdr_fwd(*s[:5], h0=s[5]) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[mm.gdr_fwd(*s[:5], h0=s[5], stream=st) for s, st in zip(sets, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    mm.mm_device_status()
+    for pair in got:
+        assert all(torch.equal(a, b) for one, ref in zip(pair, want) for a, b in zip(one, ref))
+
+
+def test_offsets_past_32_bits():
+    """v of more than 2^31 elements: the last batch row as in a call of its own."""
+    B, L, H, P, N = 9, 65600, 32, 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)
+    q, k = (torch.nn.functional.normalize(rnd(B, L, 1, N).float(), dim=-1).to(torch.bfloat16) for _ in range(2))
+    v, do = rnd(B, L, H, P), rnd(B, L, H, P)
+    g, beta = -rnd(B, L, H).abs(), rnd(B, L, H).sigmoid()
+    assert v.numel() > 2 ** 31
+    o, hT, ckpt = mm.gdr_fwd_train(q, k, v, g, beta, return_last_state=True)
+    grads = mm.gdr_bwd(q, k, v, g, beta, ckpt, do)
+    mm.mm_device_status()
+    del ckpt
+    last = [t[-1:] for t in (q, k, v, g, beta)]
+    o1, h1 = mm.gdr_fwd(*last)
+    assert torch.equal(o[-1:], o1) and torch.equal(hT[-1:], h1)
+    _, _, ckpt = mm.gdr_fwd_train(*last)
+    assert all(torch.equal(grads[n][-1:], t) for n, t in mm.gdr_bwd(*last, ckpt, do[-1:]).items())
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["forward", "backward"])
+def test_wait_runs_out(monkeypatch, backward):
+    """Nothing staged (no copy is in flight): the bounded waits give up, the status says so
+    once, and the next call is right."""
+    *qkvgb, h0 = plain.inputs(2, 130, 4, 2, 64, 128, seed=9, device="cuda", carry=True)
+    do = torch.randn(qkvgb[2].shape, device="cuda").to(torch.bfloat16)
+    call = lambda: mm.gdr_bwd(*qkvgb, ckpt, do, return_dh0=True).values() if backward else mm.gdr_fwd(*qkvgb, h0=h0)
+    _, _, ckpt = mm.gdr_fwd_train(*qkvgb, h0=h0)
+    want = [t.clone() for t in call()]
+    monkeypatch.setenv("MMSCAN_FAULT_INJECT", "stall")
+    call()
+    monkeypatch.delenv("MMSCAN_FAULT_INJECT")
+    with pytest.raises(mm.MMError) as ei:
+        mm.mm_device_status()
+    assert ei.value.name == "MM_ERR_DEVICE_TIMEOUT", str(ei.value)
+    mm.mm_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    mm.mm_device_status()
