@@ -56,7 +56,13 @@ namespace {
 // and its dg and dbeta after.
 //
 // Bound: the latency of one chunk's steps and loads (one CTA an SM: 190 KB of
-// tiles and all of TMEM at P = N = 128).
+// tiles and all of TMEM at P = N = 128; the issue slots are busy 28% of the
+// time, DRAM 36%).  Measured: 130 us for 2048 chunks of one head of 128 x 128,
+// 156 for 1040 of four heads of 64 x 128 (174 without the ring of two slots).
+// The kernel on warp-level products (mma.sync) took 174 us for the first.  Blocks
+// that stay and load the next chunk's tiles while the last one's results leave
+// measured slower (147 and 248 us): the 64 columns of dk or dq that a thread
+// holds over its heads then spill.
 constexpr int SLAB = 128 * 128;                        // 64 columns of a stacked tile
 constexpr int GEPI = 8, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
 // (B_CUM, B_ROWS: by head parity; B_RO, B_ST, B_FREE: by slot)
@@ -472,26 +478,25 @@ unsigned int read_and_clear_grad_error() {
 [[maybe_unused]] const bool g_registered = (register_error_reader(read_and_clear_grad_error), true);
 
 template <int DK, int DV>
-cudaError_t launch_grad(const GDRArgs& a, cudaStream_t s) {
+cudaError_t launch_grad(const GDRArgs& a, const CallMaps& m, cudaStream_t s) {
     constexpr int bytes = GradSmem<DK, DV>::BYTES;
-    CUtensorMap mk, mq, mv, mdo, mdk, mdq;
+    CUtensorMap mv, mdk, mdq;
     cudaError_t e;
-    if ((e = map_steps(&mk, a.k, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
-    if ((e = map_steps(&mq, a.q, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mdk, a.dk, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mdq, a.dq, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mv, a.v, DV, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
-    if ((e = map_steps(&mdo, a.dout, DV, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(gdr_bwd_grad_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    gdr_bwd_grad_kernel<DK, DV><<<(unsigned)(a.batch * a.ngroups * a.nchunks), GTHREADS, bytes, s>>>(mk, mq, mv, mdo, mdk, mdq, a);
+    static std::atomic<uint64_t> attr_done{0};
+    if ((e = allow_dynamic_smem(reinterpret_cast<const void*>(gdr_bwd_grad_kernel<DK, DV>), bytes, attr_done)) != cudaSuccess) return e;
+    gdr_bwd_grad_kernel<DK, DV><<<(unsigned)(a.batch * a.ngroups * a.nchunks), GTHREADS, bytes, s>>>(m.k, m.q, mv, m.v, mdk, mdq, a);
     return cudaGetLastError();
 }
 
 template <int DK>
 cudaError_t launch_bwd(const GDRArgs& a, cudaStream_t s) {
-    cudaError_t e = launch_gdr_chain(a, true, s);
-    if (e != cudaSuccess) return e;
-    return a.headdim == 64 ? launch_grad<DK, 64>(a, s) : launch_grad<DK, 128>(a, s);
+    CallMaps m;
+    cudaError_t e;
+    if ((e = map_call(&m, a, a.dout)) != cudaSuccess || (e = launch_gdr_chain(a, true, m, s)) != cudaSuccess) return e;
+    return a.headdim == 64 ? launch_grad<DK, 64>(a, m, s) : launch_grad<DK, 128>(a, m, s);
 }
 
 }  // namespace

@@ -534,26 +534,24 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 template <int DK, bool BWD, int PT>
-cudaError_t launch(const GDRArgs& a, cudaStream_t s) {
-    CUtensorMap mk, mq, mv, mo;
+cudaError_t launch(const GDRArgs& a, const CallMaps& m, cudaStream_t s) {
+    CUtensorMap mo;
     cudaError_t e;
-    if ((e = map_steps(&mk, a.k, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
-    if ((e = map_steps(&mq, a.q, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
-    if ((e = map_steps(&mv, BWD ? a.dout : a.v, a.headdim, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
     if ((e = map_steps(&mo, BWD ? a.dv : a.o, a.headdim, a.nheads, a.seqlen, a.batch, PT)) != cudaSuccess) return e;
     constexpr int bytes = Smem<DK>::BYTES;
-    if ((e = cudaFuncSetAttribute(gdr_chain_kernel<DK, BWD, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    gdr_chain_kernel<DK, BWD, PT><<<(unsigned)(a.batch * a.nheads * (a.headdim / PT)), NTHREADS, bytes, s>>>(mk, mq, mv, mo, a);
+    static std::atomic<uint64_t> attr_done{0};
+    if ((e = allow_dynamic_smem(reinterpret_cast<const void*>(gdr_chain_kernel<DK, BWD, PT>), bytes, attr_done)) != cudaSuccess) return e;
+    gdr_chain_kernel<DK, BWD, PT><<<(unsigned)(a.batch * a.nheads * (a.headdim / PT)), NTHREADS, bytes, s>>>(m.k, m.q, m.v, mo, a);
     return cudaGetLastError();
 }
 
 template <int DK>
-cudaError_t launch_fwd(const GDRArgs& a, cudaStream_t s) {
+cudaError_t launch_fwd(const GDRArgs& a, const CallMaps& m, cudaStream_t s) {
     // Tiles of 32 rows p where they still have an SM each: 1.72 us a chunk against
     // 2.24 (64 and 128 CTAs of one sequence of 16397 steps: 442 us against 575).
     // The checkpoint's tiles are of 64 rows, and so are the CTAs that write them.
-    if (!a.states && a.batch * a.nheads * (a.headdim / 32) <= 148) return launch<DK, false, 32>(a, s);
-    return launch<DK, false, kGdrTile>(a, s);
+    if (!a.states && a.batch * a.nheads * (a.headdim / 32) <= 148) return launch<DK, false, 32>(a, m, s);
+    return launch<DK, false, kGdrTile>(a, m, s);
 }
 
 unsigned int read_and_clear_device_error() {
@@ -568,9 +566,9 @@ unsigned int read_and_clear_device_error() {
 }  // namespace
 }  // namespace gdr
 
-cudaError_t launch_gdr_chain(const GDRArgs& a, bool backward, cudaStream_t s) {
-    if (backward) return a.dstate == 64 ? gdr::launch<64, true, kGdrTile>(a, s) : gdr::launch<128, true, kGdrTile>(a, s);
-    return a.dstate == 64 ? gdr::launch_fwd<64>(a, s) : gdr::launch_fwd<128>(a, s);
+cudaError_t launch_gdr_chain(const GDRArgs& a, bool backward, const gdr::CallMaps& m, cudaStream_t s) {
+    if (backward) return a.dstate == 64 ? gdr::launch<64, true, kGdrTile>(a, m, s) : gdr::launch<128, true, kGdrTile>(a, m, s);
+    return a.dstate == 64 ? gdr::launch_fwd<64>(a, m, s) : gdr::launch_fwd<128>(a, m, s);
 }
 
 }  // namespace mmscan

@@ -207,5 +207,18 @@ inline cudaError_t map_steps(CUtensorMap* m, const void* base, int64_t width, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The maps that a call's kernels share.
+struct CallMaps { CUtensorMap k, q, v; };                    // v: the forward's v, the backward's do
+inline cudaError_t map_call(CallMaps* m, const GDRArgs& a, const void* v) {
+    cudaError_t e;
+    if ((e = map_steps(&m->k, a.k, a.dstate, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
+    if ((e = map_steps(&m->q, a.q, a.dstate, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
+    return map_steps(&m->v, v, a.headdim, a.nheads, a.seqlen, a.batch);
+}
+
 }  // namespace gdr
+
+// The chains over the chunks, forward or backward (gdr_chain.cu).
+cudaError_t launch_gdr_chain(const GDRArgs& a, bool backward, const gdr::CallMaps& m, cudaStream_t s);
+
 }  // namespace mmscan

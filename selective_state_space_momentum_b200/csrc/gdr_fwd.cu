@@ -39,8 +39,13 @@ namespace {
 // substitution is, whatever the size of A (a product of powers of A would not
 // be: their entries grow and cancel).
 //
-// Bound: latency of the dependent steps (loads, k.k, substitution, three
-// block rows) and instruction issue, hidden by four CTAs an SM.
+// Bound: latency of the dependent steps (loads, k.k, substitution, three block
+// rows, the barriers between them) and instruction issue (a third to half of
+// the slots), hidden by four CTAs an SM.  Measured, 128 states: 8192 chunks of
+// 32 heads that share one group 72 us (2.9 TB/s of records written), 2048
+// chunks with q and k of their own 37 us.  A head a CTA: 119 us for the first;
+// the last head's store overlapped with the next one's A (Pm formed after it,
+// its decays a second time): 78.
 constexpr int MAXH = 4;                                      // heads of a CTA, at most
 struct PrepSmem {
     // K and Q (2 C DK bf16 from 0 on) until the products are formed, then:
@@ -294,16 +299,16 @@ int prep_heads(const GDRArgs& a) {
 
 template <int DK>
 cudaError_t launch_fwd(const GDRArgs& a, cudaStream_t s) {
-    CUtensorMap mk, mq;
+    CallMaps m;
     cudaError_t e;
-    if ((e = map_steps(&mk, a.k, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
-    if ((e = map_steps(&mq, a.q, DK, a.ngroups, a.seqlen, a.batch)) != cudaSuccess) return e;
+    if ((e = map_call(&m, a, a.v)) != cudaSuccess) return e;
     constexpr int bytes = PrepSmem::BYTES;
-    if ((e = cudaFuncSetAttribute(gdr_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> attr_done{0};
+    if ((e = allow_dynamic_smem(reinterpret_cast<const void*>(gdr_prep_kernel<DK>), bytes, attr_done)) != cudaSuccess) return e;
     const int nh = prep_heads(a);
-    gdr_prep_kernel<DK><<<(unsigned)(a.batch * (a.nheads / nh) * a.nchunks), 128, bytes, s>>>(mk, mq, a, nh);
+    gdr_prep_kernel<DK><<<(unsigned)(a.batch * (a.nheads / nh) * a.nchunks), 128, bytes, s>>>(m.k, m.q, a, nh);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_gdr_chain(a, false, s);
+    return launch_gdr_chain(a, false, m, s);
 }
 
 }  // namespace

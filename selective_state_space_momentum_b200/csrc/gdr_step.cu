@@ -10,7 +10,9 @@
 // the step: two dot products of a row (with k and with q, the second as
 // o = scale ((e^g S) q + u (k . q)), so that both are formed in one pass over
 // the loaded row and one shuffle reduction serves both).  All arithmetic is
-// fp32.
+// fp32.  Eight lanes a row (16 above 128 states) keep 16 states a lane in
+// flight.  Measured: 184 us for 512 requests of 32 heads of 64 x 128 (5.9 TB/s),
+// 3.1 us for one request of 32 heads of 128 x 128.
 #include "mm_common.cuh"
 #include "mm_internal.h"
 

@@ -526,27 +526,25 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float* part, int
     }
 }
 
-// The attribute is needed past 48 KB only.
-template <typename Kernel>
-cudaError_t launch_ring(Kernel kernel, int blocks, int bt, int bytes, const NormArgs& a, cudaStream_t s) {
-    if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-    }
-    kernel<<<blocks, bt, bytes, s>>>(a);
-    return cudaGetLastError();
-}
-
 template <typename IO, int VEC, int TPR, int NV, bool GATE>
 cudaError_t launch_fwd_ring(const NormArgs& a, int blocks, cudaStream_t s) {
     using R = FwdRing<norm_block(TPR), NV, VEC, GATE>;
-    return launch_ring(norm_fwd_ring_kernel<IO, VEC, TPR, NV, GATE>, blocks, norm_block(TPR), R::D * R::STAGE, a, s);
+    static std::atomic<uint64_t> attr_done{0};
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(norm_fwd_ring_kernel<IO, VEC, TPR, NV, GATE>), R::D * R::STAGE, attr_done);
+    if (e != cudaSuccess) return e;
+    norm_fwd_ring_kernel<IO, VEC, TPR, NV, GATE><<<blocks, norm_block(TPR), R::D * R::STAGE, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename IO, int VEC, int TPR, int NV, bool GATE>
 cudaError_t launch_bwd_rows(const NormArgs& a, int blocks, cudaStream_t s) {
     using R = BwdRing<norm_block(TPR), TPR, NV, VEC, GATE>;
-    return launch_ring(norm_bwd_kernel<IO, VEC, TPR, NV, GATE>, blocks, norm_block(TPR), norm_ring(VEC, TPR) ? R::D * R::STAGE : 0, a, s);
+    constexpr int bytes = norm_ring(VEC, TPR) ? R::D * R::STAGE : 0;
+    static std::atomic<uint64_t> attr_done{0};
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(norm_bwd_kernel<IO, VEC, TPR, NV, GATE>), bytes, attr_done);
+    if (e != cudaSuccess) return e;
+    norm_bwd_kernel<IO, VEC, TPR, NV, GATE><<<blocks, norm_block(TPR), bytes, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename IO, int VEC, int TPR, int NV>

@@ -2,6 +2,7 @@
 // Internal to the library (not installed, not part of the C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -388,6 +389,19 @@ __device__ __forceinline__ float softplus_f32(float v) {
     p = fmaf(p, q, 1.0f / 3.0f);
     p = fmaf(p, q, 1.0f);
     return fmaxf(v, 0.0f) + 2.0f * s * p;
+}
+
+// Host: the dynamic shared memory that `kernel` may ask for, once per device (`done`, a bit each; the default is 48 KB).
+inline cudaError_t allow_dynamic_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
 }
 
 }  // namespace mmscan

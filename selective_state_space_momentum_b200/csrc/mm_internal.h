@@ -267,8 +267,6 @@ bool gdr_shape_supported(int64_t headdim, int64_t dstate);
 cudaError_t launch_gdr_fwd(const GDRArgs& a, cudaStream_t s);
 cudaError_t launch_gdr_bwd(const GDRArgs& a, cudaStream_t s);
 cudaError_t launch_gdr_step(const GDRStepArgs& a, int io, cudaStream_t s);
-// The chain over the chunks (gdr_chain.cu), forward or backward.
-cudaError_t launch_gdr_chain(const GDRArgs& a, bool backward, cudaStream_t s);
 
 // Arguments of one layer norm call, forward or backward.
 struct NormArgs {
