@@ -754,6 +754,9 @@ typedef struct {
  * carries bf16 rounding of the products that reach it alone.  Padding a
  * batch row on the right changes nothing before the padding; its steps are
  * steps like any other for hT (give them beta = 0 and g = 0 to keep the state).
+ * A NaN or infinity in q, k or v at a step reaches all outputs of its chunk of
+ * 64 steps, those before it among them, and the chunks behind it; no chunk
+ * before it, no other batch row and (from v) no other head.
  * Streaming: calls split at a multiple of 64, with hT of the first as h0 of
  * the second, reproduce o and hT bit for bit.
  * Nothing is allocated; the calls can be captured into a CUDA graph (the

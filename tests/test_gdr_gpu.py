@@ -153,6 +153,37 @@ def test_padding_keeps_the_state_and_other_rows():
     assert all(bool(torch.isfinite(t[[0, 2]].float()).all()) for t in grads.values())
 
 
+def test_nan_stays_in_its_chunk_and_head():
+    """A NaN at a step reaches its chunk and what follows, no chunk before it and, in v, no other head."""
+    q, k, v, g, beta, _ = plain.inputs(2, 200, 4, 2, 64, 128, seed=4, device="cuda")
+    clean, _ = mm.gdr_fwd(q, k, v, g, beta)
+    bad = v.clone()
+    bad[0, 100, 1, 3] = math.nan
+    o, hT = mm.gdr_fwd(q, k, bad, g, beta)
+    assert torch.equal(o[:, :64], clean[:, :64]) and torch.equal(o[1], clean[1])
+    assert torch.equal(o[0, :, [0, 2, 3]], clean[0, :, [0, 2, 3]])
+    assert bool(torch.isnan(o[0, 100:, 1, 3].float()).all()) and bool(torch.isnan(hT[0, 1, 3]).all())
+    bad = k.clone()
+    bad[0, 100, 1, 3] = math.inf
+    o, _ = mm.gdr_fwd(q, bad, v, g, beta)
+    assert torch.equal(o[:, :64], clean[:, :64]) and torch.equal(o[1], clean[1]) and torch.equal(o[0, :, :2], clean[0, :, :2])
+    assert not bool(torch.isfinite(o[0, 101:, 2:].float()).any())
+
+
+@pytest.mark.parametrize("P", [64, 128])
+@pytest.mark.parametrize("N", [64, 128])
+def test_state_tiles_of_32_and_64_rows(P, N):
+    """Calls with fewer and with more tiles of 32 state rows than the GPU has SMs, and the
+    checkpointing call: the same bits."""
+    *qkvgb, h0 = plain.inputs(6, 150, 40, 8, P, N, seed=P + N, device="cuda", carry=True)
+    o, hT = mm.gdr_fwd(*qkvgb, h0=h0)
+    kept = mm.gdr_fwd_train(*qkvgb, h0=h0, return_last_state=True)
+    assert torch.equal(o, kept[0]) and torch.equal(hT, kept[1])
+    few = [t[:, :, h:h + n].contiguous() for t, h, n in zip(qkvgb, (2, 2, 10, 10, 10), (1, 1, 5, 5, 5))]
+    few_o, few_h = mm.gdr_fwd(*(t[4:5] for t in few), h0=h0[4:5, 10:15].contiguous())
+    assert torch.equal(o[4:5, :, 10:15], few_o) and torch.equal(hT[4:5, 10:15], few_h)
+
+
 def test_runs_are_bit_identical():
     *qkvgb, h0 = plain.inputs(2, 200, 8, 2, 128, 128, seed=3, device="cuda", carry=True)
     do = torch.randn(qkvgb[2].shape, device="cuda").to(torch.bfloat16)
