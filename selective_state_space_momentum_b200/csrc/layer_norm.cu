@@ -20,8 +20,10 @@
 // meanwhile: HBM's latency times its rate is 40 KB an SM in flight, more than
 // the registers have room for beside the row at work.  Measured against the
 // copy engine (44 us for the forward's 268 MB at 32768 rows of 2048, bf16):
-// forward 50 us, backward (402 MB) 72; with a row a block and no loop 61, with
-// the next row in registers 89.  Rows of more than 4096 columns or of no whole
+// forward 44 us, backward (402 MB) 72; with a row a block and no loop 61, with
+// the next row in registers 89.  What comes next is instruction issue (75% of
+// the slots in the forward before two fp32 operations went into one: 50 us;
+// the same in the backward measured 76 against 72).  Rows of more than 4096 columns or of no whole
 // number of 16-byte pieces, and calls of so few rows that no block has two,
 // take a row a block in the forward; the backward prefetches to registers.
 //
@@ -82,29 +84,28 @@ __device__ __forceinline__ void load_param(const float* p, float* v, float none)
     }
 }
 
-// Sum of (a, b) over the TPR threads of a row, in every one of them.  Rows of
-// more than a warp go through `red`, one of two slots that alternate from
-// call to call, so that one barrier a call is enough: a slot is written again
-// only after the barrier of the call in between.
-template <int TPR>
-__device__ __forceinline__ float2 row_sum(float2 v, float2* red, int& slot) {
+__device__ __forceinline__ float shfl_add(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
+__device__ __forceinline__ float2 shfl_add(float2 v, int m) { return f2(shfl_add(v.x, m), shfl_add(v.y, m)); }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return add2(a, b); }
+
+// Sum of v (one value, or two) over the TPR threads of a row, in every one of
+// them.  Rows of more than a warp go through `red`, one of two slots that
+// alternate from call to call, so that one barrier a call is enough: a slot is
+// written again only after the barrier of the call in between.
+template <int TPR, typename T>
+__device__ __forceinline__ T row_sum(T v, float2* red, int& slot) {
 #pragma unroll
-    for (int m = (TPR < 32 ? TPR : 32) / 2; m >= 1; m >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
-    }
+    for (int m = (TPR < 32 ? TPR : 32) / 2; m >= 1; m >>= 1) v = shfl_add(v, m);
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
-        float2* r = red + slot * W;
+        T* r = reinterpret_cast<T*>(red + slot * W);
         slot ^= 1;
         if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = make_float2(0.0f, 0.0f);
+        v = r[0];
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            v.x += r[w].x;
-            v.y += r[w].y;
-        }
+        for (int w = 1; w < W; ++w) v = plus(v, r[w]);
     }
     return v;
 }
@@ -118,6 +119,58 @@ struct Raw {
     __device__ __forceinline__ void load(const IO* p) { v = *reinterpret_cast<const decltype(v)*>(p); }
     __device__ __forceinline__ void get(float* f) const { load_vec<IO, VEC>(reinterpret_cast<const IO*>(&v), f); }
 };
+
+// A thread's elements of a row, in pairs: two fp32 operations an instruction.
+template <int K>
+__device__ __forceinline__ float2 pair(const float (&v)[K], int k) { return f2(v[k], v[k + 1]); }
+template <int K>
+__device__ __forceinline__ void put_pair(float (&v)[K], int k, float2 x) {
+    v[k] = x.x;
+    v[k + 1] = x.y;
+}
+
+// Mean and rstd of the row that v (0 past its end) is this thread's part of; v centred.
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void center(float (&v)[NV * VEC], const NormArgs& p, int t, float2* red, int& slot, float& mean, float& rstd) {
+    mean = 0.0f;
+    if (!p.rms) {
+        float2 s = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NV * VEC; k += 2) s = add2(s, pair(v, k));
+        mean = row_sum<TPR>(s.x + s.y, red, slot) * p.inv_cols;
+        const float2 off = f2(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((t + i * TPR) * VEC >= p.cols) continue;     // stays 0
+            if constexpr (VEC == 1) v[i] -= mean;
+            else
+#pragma unroll
+                for (int e = 0; e < VEC; e += 2) put_pair(v, i * VEC + e, add2(pair(v, i * VEC + e), off));
+        }
+    }
+    float2 s = f2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV * VEC; k += 2) s = fma2(pair(v, k), pair(v, k), s);
+    rstd = rsqrtf(fmaf(row_sum<TPR>(s.x + s.y, red, slot), p.inv_cols, p.eps));
+}
+
+// y of VEC of its columns: v centred, w and b and (GATE) z the columns' own.
+template <int VEC, bool GATE>
+__device__ __forceinline__ void norm_out(const float* v, float rstd, const float* w, const float* b, const float* z, float* o) {
+    if constexpr (VEC == 1) {
+        o[0] = fmaf(v[0] * rstd, w[0], b[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 y = fma2(mul2(f2(v[e], v[e + 1]), f2(rstd, rstd)), f2(w[e], w[e + 1]), f2(b[e], b[e + 1]));
+            o[e] = y.x;
+            o[e + 1] = y.y;
+        }
+    }
+    if constexpr (GATE)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] *= z[e] * sigmoid_f32(z[e]);
+}
 
 // Rows on their way: every thread copies its own pieces of 16 bytes of the next
 // rows to slots of its own in shared memory (cp.async) and reads nobody else's,
@@ -174,30 +227,14 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_fwd_resident(norm_block(
     for (int now = 0; r0 < p.rows; r0 += step, now = now + 1 == D ? 0 : now + 1) {
         cp_async_wait<D - 2>();
         const unsigned char* mine = own + now * STAGE;
-        float v[NV * VEC];
-        float2 s = make_float2(0.0f, 0.0f);
+        float v[NV * VEC], mean, rstd;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[i * VEC + e] = 0.0f;
             if ((t + i * TPR) * VEC < cols) load_vec<IO, VEC>(reinterpret_cast<const IO*>(mine + i * BT * 16), v + i * VEC);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s.x += v[i * VEC + e];
         }
-        float mean = 0.0f;
-        if (!p.rms) mean = row_sum<TPR>(s, red, slot).x * p.inv_cols;
-        s = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = (t + i * TPR) * VEC < cols;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i * VEC + e] -= mean;
-                if (in) s.x = fmaf(v[i * VEC + e], v[i * VEC + e], s.x);
-            }
-        }
-        const float var = row_sum<TPR>(s, red, slot).x * p.inv_cols;
-        const float rstd = 1.0f / sqrtf(var + p.eps);
+        center<VEC, TPR, NV>(v, p, t, red, slot, mean, rstd);
         const int64_t row = r0 + grp;
         if (row < p.rows) {
             if (t == 0) {
@@ -209,15 +246,9 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_fwd_resident(norm_block(
             for (int i = 0; i < NV; ++i) {
                 const int c = (t + i * TPR) * VEC;
                 if (c >= cols) continue;
-                float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i * VEC + e] * rstd, w[i * VEC + e], b[i * VEC + e]);
-                if constexpr (GATE) {
-                    float z[VEC];
-                    load_vec<IO, VEC>(reinterpret_cast<const IO*>(mine + (NV + i) * BT * 16), z);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) o[e] *= z[e] * sigmoid_f32(z[e]);
-                }
+                float o[VEC], z[VEC];
+                if constexpr (GATE) load_vec<IO, VEC>(reinterpret_cast<const IO*>(mine + (NV + i) * BT * 16), z);
+                norm_out<VEC, GATE>(v + i * VEC, rstd, w + i * VEC, b + i * VEC, z, o);
                 store_vec<IO, VEC>(y + c, o);
             }
         }
@@ -238,31 +269,15 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArg
     const int cols = (int)p.cols;
     const IO* x = static_cast<const IO*>(p.x) + row * cols;
 
-    float v[NV * VEC];
-    float2 s = make_float2(0.0f, 0.0f);
+    float v[NV * VEC], mean, rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * TPR) * VEC;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[i * VEC + e] = 0.0f;
         if (c < cols) load_vec<IO, VEC>(x + c, v + i * VEC);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s.x += v[i * VEC + e];
     }
-    float mean = 0.0f;
-    if (!p.rms) mean = row_sum<TPR>(s, red, slot).x * p.inv_cols;
-    s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = (t + i * TPR) * VEC < cols;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            v[i * VEC + e] -= mean;
-            if (in) s.x = fmaf(v[i * VEC + e], v[i * VEC + e], s.x);
-        }
-    }
-    const float var = row_sum<TPR>(s, red, slot).x * p.inv_cols;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
+    center<VEC, TPR, NV>(v, p, t, red, slot, mean, rstd);
     if (!active) return;
     if (t == 0) {
         if (p.mean && !p.rms) p.mean[row] = mean;
@@ -273,18 +288,16 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(const NormArg
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * TPR) * VEC;
         if (c >= cols) continue;
-        float w[VEC], b[VEC];
+        float w[VEC], b[VEC], z[VEC], o[VEC];
         load_param<VEC>(p.weight ? p.weight + c : nullptr, w, 1.0f);
         load_param<VEC>(p.bias ? p.bias + c : nullptr, b, 0.0f);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = fmaf(v[i * VEC + e] * rstd, w[e], b[e]);
         if (p.z) {
-            float z[VEC];
             load_vec<IO, VEC>(static_cast<const IO*>(p.z) + row * cols + c, z);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] *= z[e] * sigmoid_f32(z[e]);
+            norm_out<VEC, true>(v + i * VEC, rstd, w, b, z, o);
+        } else {
+            norm_out<VEC, false>(v + i * VEC, rstd, w, b, z, o);
         }
-        store_vec<IO, VEC>(y + c, w);
+        store_vec<IO, VEC>(y + c, o);
     }
 }
 
