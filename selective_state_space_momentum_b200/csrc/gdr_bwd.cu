@@ -48,23 +48,24 @@ namespace {
 //     4. Y = [r; do] S        6. Z = u dS'  (lanes 0-63)
 //        dk += tail Z - beta e^c Y, dq += scale e^c Y, and their rows' products with k and q
 // ACC stays in TMEM over the group's heads; what needs a factor of its row
-// (Y, Z) is added in registers, a thread half a row.  Products 4 and 6 run
+// (Y, Z) is added in registers, a thread a quarter of a row.  Products 4 and 6 run
 // while the epilogue forms [ad; pd].
 //
-// Roles (11 warps): 0-7 the epilogues, then one for the loads and the last
+// Roles (19 warps): 0-15 the epilogues, then one for the loads and the last
 // stores, one for the products, and one that sums up a head's decays before
 // and its dg and dbeta after.
 //
 // Bound: the latency of one chunk's steps and loads (one CTA an SM: 190 KB of
 // tiles and all of TMEM at P = N = 128; the issue slots are busy 28% of the
-// time, DRAM 36%).  Measured: 130 us for 2048 chunks of one head of 128 x 128,
-// 156 for 1040 of four heads of 64 x 128 (174 without the ring of two slots).
+// time, DRAM 36%).  Measured: 127 us for 2048 chunks of one head of 128 x 128,
+// 149 for 1040 of four heads of 64 x 128 (130 and 156 with 8 epilogue warps, 174
+// without the ring of two slots).
 // The kernel on warp-level products (mma.sync) took 174 us for the first.  Blocks
 // that stay and load the next chunk's tiles while the last one's results leave
 // measured slower (147 and 248 us): the 64 columns of dk or dq that a thread
 // holds over its heads then spill.
 constexpr int SLAB = 128 * 128;                        // 64 columns of a stacked tile
-constexpr int GEPI = 8, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
+constexpr int GEPI = 16, NP = GEPI / 4, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
 // (B_CUM, B_ROWS: by head parity; B_RO, B_ST, B_FREE: by slot)
 enum { B_QK = 0, B_G = 1, B_YZ = 2, B_YZF = 3, B_AP = 4, B_ACC = 5, B_DONE = 6, B_CUM = 7, B_ROWS = 9, B_RO = 11, B_ST = 13, B_FREE = 15, NGBAR = 17 };
 
@@ -77,9 +78,9 @@ struct GradSmem {
     static constexpr int NS = DV == 64 ? 2 : 1;
     // by head parity: the decays (double c[C], float e^(c - mid), e^(mid - c), [C]) ...
     static constexpr int CUM = SLOTS0 + NS * SLOT, CUM_BYTES = C * 8 + 2 * C * 4;
-    // ... and the sums: by column half, of dc by row of [k; q], of e^.. k.(dS' u) and of dbeta by row of k;
+    // ... and the sums: by column quarter, of dc by row of [k; q], of e^.. k.(dS' u) and of dbeta by row of k;
     // the column sums by lane quarter; <S, dS'> by warp
-    static constexpr int ROW = CUM + 2 * CUM_BYTES, ROWS = 2 * 4 * C * 4 + 4 * C * 4 + 64;
+    static constexpr int ROW = CUM + 2 * CUM_BYTES, ROWS = NP * 4 * C * 4 + 4 * C * 4 + 128;
     static constexpr int WIDE = ROW + 2 * ROWS, BAR = WIDE + 16, TSLOT = BAR + NGBAR * 8, ABORT = TSLOT + 8;
     static constexpr int BYTES = ABORT + 8 + 1024;
     static_assert(BYTES <= 227 * 1024 && U % 1024 == 0 && S % 1024 == 0 && SLOT % 1024 == 0, "shared memory");
@@ -92,7 +93,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dq, const GDRArgs p) {
     using L = GradSmem<DK, DV>;
-    constexpr int TV = DV / 64, HC = DK / 2;           // tiles of 64 p; columns of q and k a thread
+    constexpr int TV = DV / 64, HC = DK / NP;          // tiles of 64 p; columns of q and k a thread
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -234,10 +235,10 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int hh = 0; hh < hpg; ++hh) {
             if (hh + 1 < hpg) decays(hh + 1);                // its buffer was head hh - 1's, whose sums are taken
             if (!wwait(B_ROWS + (hh & 1), hh >> 1)) break;
-            const float* rowc = reinterpret_cast<const float*>(sm + L::ROW + (hh & 1) * L::ROWS);   // [half][128]
-            const float* rowk = rowc + 4 * C;                                                      // [half][C]
-            const float* rowb = rowk + 2 * C;
-            const float* colv = rowb + 2 * C;                                                      // [quarter][C]
+            const float* rowc = reinterpret_cast<const float*>(sm + L::ROW + (hh & 1) * L::ROWS);   // [part][128]
+            const float* rowk = rowc + NP * 2 * C;                                                 // [part][C]
+            const float* rowb = rowk + NP * C;
+            const float* colv = rowb + NP * C;                                                     // [quarter][C]
             const float* red = colv + 4 * C;                                                       // [warp], then e^(c_last)
             float dc[2], ok[2], db[2], sums = 0.0f;
 #pragma unroll
@@ -245,9 +246,14 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const int i = 2 * lane + e;
                 float col = colv[C + i] + colv[3 * C + i];   // rows 32-63 of k and of q
                 if (i < 32) col += colv[i] + colv[2 * C + i];
-                ok[e] = rowk[i] + rowk[C + i];
-                db[e] = rowb[i] + rowb[C + i];
-                dc[e] = rowc[i] + rowc[2 * C + i] + rowc[C + i] + rowc[3 * C + i] - col - ok[e];
+                ok[e] = db[e] = dc[e] = 0.0f;
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+                    ok[e] += rowk[m * C + i];
+                    db[e] += rowb[m * C + i];
+                    dc[e] += rowc[2 * m * C + i] + rowc[(2 * m + 1) * C + i];
+                }
+                dc[e] -= col + ok[e];
                 sums += ok[e];
             }
 #pragma unroll
@@ -280,12 +286,12 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
         }
     } else {
-        const int q = w & 3, half = w >> 2;
+        const int q = w & 3, part = w >> 2;
         const int t = 32 * q + lane, i = t & 63;             // TMEM lane: row of [k; q]; step of the chunk
         const bool krows = q < 2;
-        const bool below = (q & 1) != 0 || half == 0;        // this warp's 32 x 32 of [ad; pd] reaches the triangle
+        const bool below = (q & 1) != 0 || part < NP / 2;    // this warp's 32 x 16 of [ad; pd] reaches the triangle
         const uint32_t lb = tmem + ((uint32_t)(q * 32) << 16);
-        const int c0 = HC * half;                            // this thread's columns of q and k
+        const int c0 = HC * part;                            // this thread's columns of q and k
         float2 acc[HC / 2];
 #pragma unroll
         for (int e = 0; e < HC / 2; ++e) acc[e] = f2(0.0f, 0.0f);
@@ -297,16 +303,17 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const unsigned char* slot = sm + L::SLOTS0 + sl * L::SLOT;
             const float* f = reinterpret_cast<const float*>(slot + L::F);
             float* rowc = reinterpret_cast<float*>(sm + L::ROW + (hh & 1) * L::ROWS);
-            float* rowk = rowc + 4 * C;
-            float* rowb = rowk + 2 * C;
-            float* colv = rowb + 2 * C;
+            float* rowk = rowc + NP * 2 * C;
+            float* rowb = rowk + NP * C;
+            float* colv = rowb + NP * C;
             float* red = colv + 4 * C;
             float rc = 0.0f, rk = 0.0f, rb = 0.0f;
             if (!(ok = wwait(B_CUM + (hh & 1), hh >> 1) && wwait(B_RO + sl, hh / L::NS) && (hh == 0 || wwait(B_ACC, hh - 1)))) break;
             const float eg = f[i], tail = f[C + i], beta = f[2 * C + i];
-            if (krows) {                                     // r.v over this thread's half of p
+            if (krows) {                                     // r.v over this thread's part of p
 #pragma unroll
-                for (int x = half * (DV / 16); x < (half + 1) * (DV / 16); ++x) {
+                for (int n = 0; n < DV / 8 / NP; ++n) {
+                    const int x = part * (DV / 8 / NP) + n;
                     const uint4 vv = *reinterpret_cast<const uint4*>(slot + L::V + (x >> 3) * (SLAB / 2) + tile_off<128>(i, x & 7));
                     const uint4 rr = *reinterpret_cast<const uint4*>(slot + L::RO + (x >> 3) * SLAB + tile_off<128>(i, x & 7));
                     rb = fmaf(bf16_lo(vv.x), bf16_lo(rr.x), fmaf(bf16_hi(vv.x), bf16_hi(rr.x), rb));
@@ -317,27 +324,24 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             if (!(ok = wwait(B_G, hh))) break;
             tc_fence_after();
-            uint32_t ap[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ap[e] = 0u;
             if (below) {
-                uint32_t g[32], kq[32];
-                tmem_ld32(lb + TG_G + 32 * half, g);
-                tmem_ld32(lb + TG_KQ + 32 * half, kq);
+                uint32_t g[16], kq[16], ap[8];
+                tmem_ld16(lb + TG_G + 16 * part, g);
+                tmem_ld16(lb + TG_KQ + 16 * part, kq);
                 tmem_wait_ld();
                 // d: what multiplies r.u (minus the decay) or do.u (scale times it)
                 const float row = (krows ? -1.0f : p.scale) * ef[i];
                 const bool apart = wide[hh & 1] != 0;
-                float wv[32];
+                float wv[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 fj = *reinterpret_cast<const float4*>(ef + C + 32 * half + e);
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 fj = *reinterpret_cast<const float4*>(ef + C + 16 * part + e);
                     float d[4] = {row * fj.x, row * fj.y, row * fj.z, row * fj.w};
                     if (apart) {
                         const float sgn = krows ? -1.0f : p.scale;
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
-                            const int j = 32 * half + e + k;
+                            const int j = 16 * part + e + k;
                             const float x = j <= i ? sgn * ex2_approx((float)((cum[i] - cum[j]) * kLog2e)) : 0.0f;
                             d[0] = k == 0 ? x : d[0];
                             d[1] = k == 1 ? x : d[1];
@@ -348,7 +352,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     float a[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int j = 32 * half + e + k;
+                        const int j = 16 * part + e + k;
                         const float x = (krows ? j < i : j <= i) ? d[k] * __uint_as_float(g[e + k]) : 0.0f;
                         const float s = __uint_as_float(kq[e + k]);
                         if (krows) rb = fmaf(x, s, rb);
@@ -360,17 +364,18 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     ap[e / 2 + 1] = pack_bf16x2(a[2], a[3]);
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 4 * half + c)) = make_uint4(ap[4 * c], ap[4 * c + 1], ap[4 * c + 2], ap[4 * c + 3]);
+                for (int c = 0; c < 2; ++c)
+                    *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 2 * part + c)) = make_uint4(ap[4 * c], ap[4 * c + 1], ap[4 * c + 2], ap[4 * c + 3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 arrive(B_AP);
                 float col[1];
-                butterfly_sum<32, 32>(wv, col, lane);        // lane j: the sum of column j over the warp's rows
-                colv[q * C + 32 * half + lane] = col[0];
+                butterfly_sum<16, 16>(wv, col, lane & 15);   // lanes j, j + 16: column j's sum over half the warp's rows each
+                col[0] += __shfl_xor_sync(0xffffffffu, col[0], 16);
+                if (lane < 16) colv[q * C + 16 * part + lane] = col[0];
             } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 4 * half + c)) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 2 * part + c)) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 arrive(B_AP);
             }
@@ -390,20 +395,20 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (lane == 0) red[w] = sd;
             if (tid == 0) red[GEPI] = f[C - 1];
             arrive(B_FREE + sl);
-            // Y and Z, 32 columns at a time
+            // Y and Z, 16 columns at a time
             if (!(ok = wwait(B_YZ, hh))) break;
             tc_fence_after();
             float dy = 0.0f, dz = 0.0f;
             const float fy = krows ? -beta * eg : p.scale * eg;
 #pragma unroll
-            for (int cc = 0; cc < HC / 32; ++cc) {
-                const int col = c0 + 32 * cc;
-                uint32_t y[32], z[32];
-                tmem_ld32(lb + TG_Y + col, y);
-                if (krows) tmem_ld32(lb + TG_Z + col, z);
+            for (int cc = 0; cc < HC / 16; ++cc) {
+                const int col = c0 + 16 * cc;
+                uint32_t y[16], z[16];
+                tmem_ld16(lb + TG_Y + col, y);
+                if (krows) tmem_ld16(lb + TG_Z + col, z);
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     const uint4 row = *reinterpret_cast<const uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c));
                     const uint32_t r4[4] = {row.x, row.y, row.z, row.w};
 #pragma unroll
@@ -411,7 +416,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         const int k = 8 * c + 2 * e;
                         const float2 yy = f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
                         const float2 kk = f2(bf16_lo(r4[e]), bf16_hi(r4[e]));
-                        float2& a = acc[16 * cc + k / 2];
+                        float2& a = acc[8 * cc + k / 2];
                         a = fma2(f2(fy, fy), yy, a);
                         dy = fmaf(yy.x, kk.x, fmaf(yy.y, kk.y, dy));
                         if (krows) {
@@ -428,28 +433,28 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (krows) {
                 rk = tail * dz;
                 rb = fmaf(-eg, dy, rb);
-                rowk[half * C + i] = rk;
-                rowb[half * C + i] = rb;
+                rowk[part * C + i] = rk;
+                rowb[part * C + i] = rb;
             }
-            rowc[half * 2 * C + t] = rc;
+            rowc[part * 2 * C + t] = rc;
             arrive(B_ROWS + (hh & 1));
         }
         // dk, dq into the tile of k and q
         if (ok && wwait(B_ACC, hpg - 1)) {
             tc_fence_after();
 #pragma unroll
-            for (int cc = 0; cc < HC / 32; ++cc) {
-                const int col = c0 + 32 * cc;
-                uint32_t y[32];
-                tmem_ld32(lb + TG_ACC + col, y);
+            for (int cc = 0; cc < HC / 16; ++cc) {
+                const int col = c0 + 16 * cc;
+                uint32_t y[16];
+                tmem_ld16(lb + TG_ACC + col, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int k = 8 * c + 2 * e;
-                        const float2 a = add2(acc[16 * cc + k / 2], f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
+                        const float2 a = add2(acc[8 * cc + k / 2], f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
                         o[e] = pack_bf16x2(a.x, a.y);
                     }
                     *reinterpret_cast<uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c)) = make_uint4(o[0], o[1], o[2], o[3]);
