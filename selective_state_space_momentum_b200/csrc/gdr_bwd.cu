@@ -39,31 +39,32 @@ namespace gdr {
 namespace {
 
 // ------------------------------------------------- everything else, by chunk ----
-// One CTA a batch row, group and chunk, on tensor cores (tcgen05 / TMEM).  As
-// in the chain, k and q are stacked into one tile of 128 rows, and so are r
-// and do: of every product the rows of k and dk are lanes 0-63, those of q
-// and dq lanes 64-127.  Per head of the group:
+// One CTA an SM, on tensor cores (tcgen05 / TMEM); it goes from item to item (a
+// batch row, group and chunk), the next one's first tiles loading while the
+// last one's results leave.  As in the chain, k and q are stacked into one tile
+// of 128 rows, and so are r and do: of every product the rows of k and dk are
+// lanes 0-63, those of q and dq lanes 64-127.  Per head of the group:
 //     1. [k; q] k^T (once)    2. [r; do] u^T     -> [ad; pd], the row and column sums of W
 //     3. ACC += [ad; pd] k    5. ACC += [ad; pd]^T [k; q]  (lanes 0-63; zeros below)
 //     4. Y = [r; do] S        6. Z = u dS'  (lanes 0-63)
 //        dk += tail Z - beta e^c Y, dq += scale e^c Y, and their rows' products with k and q
 // ACC stays in TMEM over the group's heads; what needs a factor of its row
-// (Y, Z) is added in registers, a thread a quarter of a row.  Products 4 and 6 run
-// while the epilogue forms [ad; pd].
+// (Y, Z) the epilogue adds to it there, a thread a quarter of a row (held in
+// registers instead, the sums spill, and with the shared memory in use what
+// spills goes to L2: 147 us against 100).  Products 4 and 6 run while the
+// epilogue forms [ad; pd], after 1 and 2.
 //
-// Roles (19 warps): 0-15 the epilogues, then one for the loads and the last
-// stores, one for the products, and one that sums up a head's decays before
-// and its dg and dbeta after.
+// Roles (19 warps): 0-15 the epilogues, then one for the loads and the stores,
+// one for the products, and one that sums up a head's decays before and its dg
+// and dbeta after.  Loads are issued in the order of need, k and q (into the
+// tile that the last item's dq and dk leave from) before S and dS'.
 //
-// Bound: the latency of one chunk's steps and loads (one CTA an SM: 190 KB of
-// tiles and all of TMEM at P = N = 128; the issue slots are busy 28% of the
-// time, DRAM 36%).  Measured: 127 us for 2048 chunks of one head of 128 x 128,
-// 149 for 1040 of four heads of 64 x 128 (130 and 156 with 8 epilogue warps, 174
-// without the ring of two slots).
-// The kernel on warp-level products (mma.sync) took 174 us for the first.  Blocks
-// that stay and load the next chunk's tiles while the last one's results leave
-// measured slower (147 and 248 us): the 64 columns of dk or dq that a thread
-// holds over its heads then spill.
+// Bound: the latency of one chunk's steps (one CTA an SM: 190 KB of tiles and
+// all of TMEM at P = N = 128): the last item's store, k and q, two products,
+// [ad; pd], two products, the sums.  Measured: 100 us for 2048 chunks of one head
+// of 128 x 128, 141 for 1040 of four heads of 64 x 128.  A CTA an item took 127
+// and 149 us, with 8 epilogue warps 130 and 156; warp-level products (mma.sync)
+// 174 for the first.  Products 3 and 5 before 4 and 6: 108 and 140 us.
 constexpr int SLAB = 128 * 128;                        // 64 columns of a stacked tile
 constexpr int GEPI = 16, NP = GEPI / 4, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
 // (B_CUM, B_ROWS: by head parity; B_RO, B_ST, B_FREE: by slot)
@@ -99,11 +100,20 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     unsigned char* sm = smem_raw + (base - raw_addr);
     const int tid = threadIdx.x, lane = tid & 31, w = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int64_t ch = blockIdx.x % p.nchunks, bg = blockIdx.x / p.nchunks;
-    const int64_t b = bg / p.ngroups, grp = bg - b * p.ngroups;
-    const int hpg = (int)(p.nheads / p.ngroups), h0 = (int)grp * hpg;
-    const int64_t t0 = ch * C;
-    const int valid = (int)(p.seqlen - t0 < C ? p.seqlen - t0 : C);
+    // The block's items m = 0 .. items - 1; their heads count on as n = 0 .. heads - 1.
+    const int64_t all = p.batch * p.ngroups * p.nchunks;
+    const int hpg = (int)(p.nheads / p.ngroups), items = (int)((all - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    const int heads = items * hpg;                            // (batch * nheads * chunks < 2^31)
+    struct Item { int64_t b; int grp, t0; int64_t ch; };
+    auto item_of = [&](int m) {
+        const int64_t it = blockIdx.x + (int64_t)m * gridDim.x, bg = it / p.nchunks;
+        Item x;
+        x.ch = it - bg * p.nchunks;
+        x.b = bg / p.ngroups;
+        x.grp = (int)(bg - x.b * p.ngroups);
+        x.t0 = (int)(x.ch * C);
+        return x;
+    };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::ABORT);
     int* wide = reinterpret_cast<int*>(sm + L::WIDE);
     auto bar = [&](int i) { return base + L::BAR + 8u * (uint32_t)i; };
@@ -135,91 +145,106 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     };
 
     if (w == G_LOAD) {
-        if (lane == 0) {
-            bool live = true;
-            for (int hh = 0; hh < hpg && !p.stall; ++hh) {   // (stall: test only, nothing staged, every wait runs out)
-                const int sl = hh % L::NS;
-                if (hh >= L::NS && !(live = wait(B_FREE + sl, hh / L::NS - 1))) break;
-                const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = bar(B_RO + sl), st = bar(B_ST + sl);
-                const int h = h0 + hh;
-                const int64_t rec = (b * p.nheads + h) * p.nchunks + ch;
-                if (hh == 0) {
-                    mbar_expect_tx(bar(B_QK), DK / 64 * SLAB);
-#pragma unroll
-                    for (int s = 0; s < DK / 64; ++s) {
-                        tma_load_4d(base + L::KQ + s * SLAB, &tm_k, bar(B_QK), 64 * s, (int)grp, (int)t0, (int)b);
-                        tma_load_4d(base + L::KQ + s * SLAB + SLAB / 2, &tm_q, bar(B_QK), 64 * s, (int)grp, (int)t0, (int)b);
-                    }
-                }
-                mbar_expect_tx(ro, TV * 2 * SLAB + 3 * C * 4);
-#pragma unroll
-                for (int t = 0; t < TV; ++t) {
-                    bulk_load(slot + L::RO + t * SLAB, static_cast<const unsigned char*>(p.dr) + (rec * TV + t) * (SLAB / 2), SLAB / 2, ro);
-                    tma_load_4d(slot + L::RO + t * SLAB + SLAB / 2, &tm_do, ro, 64 * t, h, (int)t0, (int)b);
-                    tma_load_4d(slot + L::V + t * (SLAB / 2), &tm_v, ro, 64 * t, h, (int)t0, (int)b);
-                }
-                bulk_load(slot + L::U, static_cast<const unsigned char*>(p.u) + rec * TV * (SLAB / 2), TV * (SLAB / 2), ro);
-                bulk_load(slot + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, ro);
-                mbar_expect_tx(st, 2 * DV * DK * 2);
-                bulk_load(slot + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * DK * 2, DV * DK * 2, st);
-                bulk_load(slot + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * DK * 2, DV * DK * 2, st);
-            }
-            // dq, dk, staged in the tile of k and q (rows past L are clipped)
-            if (live && wait(B_DONE, 0)) {
+        if (lane == 0 && !p.stall) {                         // (stall: test only, nothing staged, every wait runs out)
+            // dq, dk of item m, staged in the tile of k and q (rows past L are clipped)
+            auto store = [&](int m) -> bool {
+                if (!wait(B_DONE, m)) return false;
+                const Item x = item_of(m);
 #pragma unroll
                 for (int s = 0; s < DK / 64; ++s) {
-                    tma_store_4d(&tm_dk, base + L::KQ + s * SLAB, 64 * s, (int)grp, (int)t0, (int)b);
-                    tma_store_4d(&tm_dq, base + L::KQ + s * SLAB + SLAB / 2, 64 * s, (int)grp, (int)t0, (int)b);
+                    tma_store_4d(&tm_dk, base + L::KQ + s * SLAB, 64 * s, x.grp, x.t0, (int)x.b);
+                    tma_store_4d(&tm_dq, base + L::KQ + s * SLAB + SLAB / 2, 64 * s, x.grp, x.t0, (int)x.b);
                 }
                 bulk_commit_group();
+                bulk_wait_read_all();
+                return true;
+            };
+            bool live = true;
+            int n = 0;
+            for (int m = 0; m < items && live; ++m) {
+                const Item x = item_of(m);
+                for (int hh = 0; hh < hpg; ++hh, ++n) {
+                    const int sl = n % L::NS, h = x.grp * hpg + hh;
+                    if (n >= L::NS && !(live = wait(B_FREE + sl, n / L::NS - 1))) break;
+                    const int64_t rec = (x.b * p.nheads + h) * p.nchunks + x.ch;
+                    const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = bar(B_RO + sl), st = bar(B_ST + sl);
+                    mbar_expect_tx(ro, TV * 2 * SLAB + 3 * C * 4);
+#pragma unroll
+                    for (int t = 0; t < TV; ++t) {
+                        bulk_load(slot + L::RO + t * SLAB, static_cast<const unsigned char*>(p.dr) + (rec * TV + t) * (SLAB / 2), SLAB / 2, ro);
+                        tma_load_4d(slot + L::RO + t * SLAB + SLAB / 2, &tm_do, ro, 64 * t, h, x.t0, (int)x.b);
+                        tma_load_4d(slot + L::V + t * (SLAB / 2), &tm_v, ro, 64 * t, h, x.t0, (int)x.b);
+                    }
+                    bulk_load(slot + L::U, static_cast<const unsigned char*>(p.u) + rec * TV * (SLAB / 2), TV * (SLAB / 2), ro);
+                    bulk_load(slot + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, ro);
+                    if (hh == 0) {                           // k and q, once the tile has given up the last item's dq and dk: before
+                                                             // S and dS', which are needed last (a store queues behind the loads)
+                        if (m > 0 && !(live = store(m - 1))) break;
+                        mbar_expect_tx(bar(B_QK), DK / 64 * SLAB);
+#pragma unroll
+                        for (int s = 0; s < DK / 64; ++s) {
+                            tma_load_4d(base + L::KQ + s * SLAB, &tm_k, bar(B_QK), 64 * s, x.grp, x.t0, (int)x.b);
+                            tma_load_4d(base + L::KQ + s * SLAB + SLAB / 2, &tm_q, bar(B_QK), 64 * s, x.grp, x.t0, (int)x.b);
+                        }
+                    }
+                    mbar_expect_tx(st, 2 * DV * DK * 2);
+                    bulk_load(slot + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * DK * 2, DV * DK * 2, st);
+                    bulk_load(slot + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * DK * 2, DV * DK * 2, st);
+                }
             }
-            bulk_wait_all();                                 // complete before the CTA exits
+            if (live) store(items - 1);                      // (read out of shared memory: it is the kernel's end that completes it)
         }
     } else if (w == G_MMA) {
         const uint32_t kq = base + L::KQ, ap = base + L::AP;
         constexpr uint32_t ID64 = umma_idesc_bf16(128, 64, 0, 0), IDKK = umma_idesc_bf16(128, DK, 0, 0),
                            IDKN = umma_idesc_bf16(128, DK, 0, 1), IDNN = umma_idesc_bf16(128, DK, 1, 1);
         auto kmaj = [&](uint32_t tile, int s, uint32_t stride) { return umma_desc_sw128(tile + (s >> 2) * stride + (s & 3) * 32, 16, 1024); };
-        bool live = wwait(B_QK, 0);
-        if (live) {
-            tc_fence_after();
+        bool live = true;
+        int n = 0;
+        for (int m = 0; m < items && live; ++m) {
+            for (int hh = 0; hh < hpg; ++hh, ++n) {
+                const int sl = n % L::NS, ph = (n & 1);
+                const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = slot + L::RO, u = slot + L::U;
+                if (!(live = wwait(B_RO + sl, n / L::NS))) break;
+                tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < DK / 16; ++s) umma_elect(tmem + TG_KQ, kmaj(kq, s, SLAB), kmaj(kq, s, SLAB), ID64, s > 0);
+                for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_G, kmaj(ro, s, SLAB), kmaj(u, s, SLAB / 2), ID64, s > 0);
+                if (hh == 0) {                               // k and q come after the last item's results have left
+                    if (!(live = wwait(B_QK, m))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < DK / 16; ++s) umma_elect(tmem + TG_KQ, kmaj(kq, s, SLAB), kmaj(kq, s, SLAB), ID64, s > 0);
+                }
+                commit_elect(bar(B_G));
+                if (!(live = wwait(B_ST + sl, n / L::NS) && (n == 0 || wwait(B_YZF, ph ^ 1)))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Y, kmaj(ro, s, SLAB), kmaj(slot + L::S, s, DK * 128), IDKK, s > 0);
+#pragma unroll
+                for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Z, kmaj(u, s, SLAB / 2), kmaj(slot + L::DS, s, DK * 128), IDKK, s > 0);
+                commit_elect(bar(B_YZ));
+                commit_elect(bar(B_FREE + sl));
+                if (!(live = wwait(B_AP, ph))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < C / 16; ++s)
+                    umma_elect(tmem + TG_ACC, kmaj(ap, s, 0), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDKN, hh > 0 || s > 0);
+#pragma unroll
+                for (int s = 0; s < 2 * C / 16; ++s)
+                    umma_elect(tmem + TG_ACC, umma_desc_sw128(ap + s * 2048, L::Z0 - L::AP, 1024), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDNN, 1u);
+                commit_elect(bar(B_ACC));
+            }
         }
-        for (int hh = 0; hh < hpg && live; ++hh) {
-            const int sl = hh % L::NS;
-            const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = slot + L::RO, u = slot + L::U;
-            if (!(live = wwait(B_RO + sl, hh / L::NS))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_G, kmaj(ro, s, SLAB), kmaj(u, s, SLAB / 2), ID64, s > 0);
-            commit_elect(bar(B_G));
-            if (!(live = wwait(B_ST + sl, hh / L::NS) && (hh == 0 || wwait(B_YZF, hh - 1)))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Y, kmaj(ro, s, SLAB), kmaj(slot + L::S, s, DK * 128), IDKK, s > 0);
-#pragma unroll
-            for (int s = 0; s < DV / 16; ++s) umma_elect(tmem + TG_Z, kmaj(u, s, SLAB / 2), kmaj(slot + L::DS, s, DK * 128), IDKK, s > 0);
-            commit_elect(bar(B_YZ));
-            commit_elect(bar(B_FREE + sl));
-            if (!(live = wwait(B_AP, hh))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < C / 16; ++s)
-                umma_elect(tmem + TG_ACC, kmaj(ap, s, 0), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDKN, hh > 0 || s > 0);
-#pragma unroll
-            for (int s = 0; s < 2 * C / 16; ++s)
-                umma_elect(tmem + TG_ACC, umma_desc_sw128(ap + s * 2048, L::Z0 - L::AP, 1024), umma_desc_sw128(kq + s * 2048, SLAB, 1024), IDNN, 1u);
-            commit_elect(bar(B_ACC));
-        }
-        if (live) wwait(B_ACC, hpg - 1);                     // the last commit must land before the CTA may exit
+        if (live) wwait(B_ACC, (heads - 1) & 1);             // the last commit must land before the CTA may exit
     } else if (w == G_AUX) {
-        auto decays = [&](int hh) {
-            double* cum = reinterpret_cast<double*>(sm + L::CUM + (hh & 1) * L::CUM_BYTES);
+        auto decays = [&](int n) {
+            const Item x = item_of(n / hpg);
+            const int h = x.grp * hpg + n % hpg, valid = (int)(p.seqlen - x.t0 < C ? p.seqlen - x.t0 : C);
+            double* cum = reinterpret_cast<double*>(sm + L::CUM + (n & 1) * L::CUM_BYTES);
             float* ef = reinterpret_cast<float*>(cum + C);
             const int r = 2 * lane;
             double s0, s1, last;
-            chunk_cumsum(static_cast<const bf16*>(p.g) + (b * p.seqlen + t0) * p.nheads + h0 + hh, p.nheads, valid, lane, s0, s1, last);
+            chunk_cumsum(static_cast<const bf16*>(p.g) + (x.b * p.seqlen + x.t0) * p.nheads + h, p.nheads, valid, lane, s0, s1, last);
             cum[r] = s0;
             cum[r + 1] = s1;
             // factors of e^(c_i - c_j), or ones (and then by element), as in the preparing kernel
@@ -228,14 +253,16 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const bool far = __any_sync(0xffffffffu, !(fabs(a0) < 60.0) || !(fabs(a1) < 60.0));
             *reinterpret_cast<float2*>(ef + r) = far ? f2(1.0f, 1.0f) : f2(ex2_approx((float)a0), ex2_approx((float)a1));
             *reinterpret_cast<float2*>(ef + C + r) = far ? f2(1.0f, 1.0f) : f2(ex2_approx((float)-a0), ex2_approx((float)-a1));
-            if (lane == 0) wide[hh & 1] = far;
-            arrive(B_CUM + (hh & 1));
+            if (lane == 0) wide[n & 1] = far;
+            arrive(B_CUM + (n & 1));
         };
         decays(0);
-        for (int hh = 0; hh < hpg; ++hh) {
-            if (hh + 1 < hpg) decays(hh + 1);                // its buffer was head hh - 1's, whose sums are taken
-            if (!wwait(B_ROWS + (hh & 1), hh >> 1)) break;
-            const float* rowc = reinterpret_cast<const float*>(sm + L::ROW + (hh & 1) * L::ROWS);   // [part][128]
+        for (int n = 0; n < heads; ++n) {
+            if (n + 1 < heads) decays(n + 1);                // its buffer was head n - 1's, whose sums are taken
+            if (!wwait(B_ROWS + (n & 1), n >> 1)) break;
+            const Item x = item_of(n / hpg);
+            const int h = x.grp * hpg + n % hpg, valid = (int)(p.seqlen - x.t0 < C ? p.seqlen - x.t0 : C);
+            const float* rowc = reinterpret_cast<const float*>(sm + L::ROW + (n & 1) * L::ROWS);   // [part][128]
             const float* rowk = rowc + NP * 2 * C;                                                 // [part][C]
             const float* rowb = rowk + NP * C;
             const float* colv = rowb + NP * C;                                                     // [quarter][C]
@@ -273,7 +300,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (lane + m < 32) run += dn;
             }
             const float after = run - dc[0];
-            const int64_t at = (b * p.seqlen + t0 + 2 * lane) * p.nheads + h0 + hh;
+            const int64_t at = (x.b * p.seqlen + x.t0 + 2 * lane) * p.nheads + h;
             bf16* dg = static_cast<bf16*>(p.dg);
             bf16* dbeta = static_cast<bf16*>(p.dbeta);
             if (2 * lane < valid) {
@@ -292,28 +319,30 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const bool below = (q & 1) != 0 || part < NP / 2;    // this warp's 32 x 16 of [ad; pd] reaches the triangle
         const uint32_t lb = tmem + ((uint32_t)(q * 32) << 16);
         const int c0 = HC * part;                            // this thread's columns of q and k
-        float2 acc[HC / 2];
-#pragma unroll
-        for (int e = 0; e < HC / 2; ++e) acc[e] = f2(0.0f, 0.0f);
         bool ok = true;
-        for (int hh = 0; hh < hpg; ++hh) {
-            const double* cum = reinterpret_cast<const double*>(sm + L::CUM + (hh & 1) * L::CUM_BYTES);
+        int hh = 0, m = 0;
+        for (int n = 0; n < heads; ++n, ++hh) {
+            if (hh == hpg) {
+                hh = 0;
+                ++m;
+            }
+            const int sl = n % L::NS, ph = (n & 1);
+            const double* cum = reinterpret_cast<const double*>(sm + L::CUM + ph * L::CUM_BYTES);
             const float* ef = reinterpret_cast<const float*>(cum + C);
-            const int sl = hh % L::NS;
             const unsigned char* slot = sm + L::SLOTS0 + sl * L::SLOT;
             const float* f = reinterpret_cast<const float*>(slot + L::F);
-            float* rowc = reinterpret_cast<float*>(sm + L::ROW + (hh & 1) * L::ROWS);
+            float* rowc = reinterpret_cast<float*>(sm + L::ROW + ph * L::ROWS);
             float* rowk = rowc + NP * 2 * C;
             float* rowb = rowk + NP * C;
             float* colv = rowb + NP * C;
             float* red = colv + 4 * C;
             float rc = 0.0f, rk = 0.0f, rb = 0.0f;
-            if (!(ok = wwait(B_CUM + (hh & 1), hh >> 1) && wwait(B_RO + sl, hh / L::NS) && (hh == 0 || wwait(B_ACC, hh - 1)))) break;
+            if (!(ok = wwait(B_CUM + ph, n >> 1) && wwait(B_RO + sl, n / L::NS))) break;
             const float eg = f[i], tail = f[C + i], beta = f[2 * C + i];
             if (krows) {                                     // r.v over this thread's part of p
 #pragma unroll
-                for (int n = 0; n < DV / 8 / NP; ++n) {
-                    const int x = part * (DV / 8 / NP) + n;
+                for (int m = 0; m < DV / 8 / NP; ++m) {
+                    const int x = part * (DV / 8 / NP) + m;
                     const uint4 vv = *reinterpret_cast<const uint4*>(slot + L::V + (x >> 3) * (SLAB / 2) + tile_off<128>(i, x & 7));
                     const uint4 rr = *reinterpret_cast<const uint4*>(slot + L::RO + (x >> 3) * SLAB + tile_off<128>(i, x & 7));
                     rb = fmaf(bf16_lo(vv.x), bf16_lo(rr.x), fmaf(bf16_hi(vv.x), bf16_hi(rr.x), rb));
@@ -322,7 +351,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     rb = fmaf(bf16_lo(vv.w), bf16_lo(rr.w), fmaf(bf16_hi(vv.w), bf16_hi(rr.w), rb));
                 }
             }
-            if (!(ok = wwait(B_G, hh))) break;
+            if (!(ok = wwait(B_G, ph))) break;
             tc_fence_after();
             if (below) {
                 uint32_t g[16], kq[16], ap[8];
@@ -331,7 +360,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 tmem_wait_ld();
                 // d: what multiplies r.u (minus the decay) or do.u (scale times it)
                 const float row = (krows ? -1.0f : p.scale) * ef[i];
-                const bool apart = wide[hh & 1] != 0;
+                const bool apart = wide[ph] != 0;
                 float wv[16];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
@@ -377,10 +406,11 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(sm + L::AP + tile_off<128>(t, 2 * part + c)) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
+                tc_fence_before();
                 arrive(B_AP);
             }
             // <S, dS'>: both tiles have the same layout
-            if (!(ok = wwait(B_ST + sl, hh / L::NS))) break;
+            if (!(ok = wwait(B_ST + sl, n / L::NS))) break;
             float sd = 0.0f;
 #pragma unroll 4
             for (int x = tid; x < DV * DK / 8; x += 32 * GEPI) {
@@ -391,44 +421,57 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 sd = fmaf(bf16_lo(a.w), bf16_lo(d.w), fmaf(bf16_hi(a.w), bf16_hi(d.w), sd));
             }
 #pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
+            for (int x = 16; x >= 1; x >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, x);
             if (lane == 0) red[w] = sd;
             if (tid == 0) red[GEPI] = f[C - 1];
             arrive(B_FREE + sl);
-            // Y and Z, 16 columns at a time
-            if (!(ok = wwait(B_YZ, hh))) break;
+            // Y and Z, 16 columns at a time, onto ACC: back to TMEM for the group's next
+            // head, or as dk and dq into the tile of k and q (of which a thread reads
+            // and writes the same elements; the products have read them)
+            if (!(ok = wwait(B_YZ, ph) && wwait(B_ACC, ph) && (hh > 0 || wwait(B_QK, m)))) break;
             tc_fence_after();
             float dy = 0.0f, dz = 0.0f;
             const float fy = krows ? -beta * eg : p.scale * eg;
+            const bool last = hh + 1 == hpg;
 #pragma unroll
             for (int cc = 0; cc < HC / 16; ++cc) {
                 const int col = c0 + 16 * cc;
-                uint32_t y[16], z[16];
+                uint32_t y[16], z[16], a[16];
                 tmem_ld16(lb + TG_Y + col, y);
+                tmem_ld16(lb + TG_ACC + col, a);
                 if (krows) tmem_ld16(lb + TG_Z + col, z);
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint4 row = *reinterpret_cast<const uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c));
+                    uint4* at = reinterpret_cast<uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c));
+                    const uint4 row = *at;
                     const uint32_t r4[4] = {row.x, row.y, row.z, row.w};
+                    uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int k = 8 * c + 2 * e;
                         const float2 yy = f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
                         const float2 kk = f2(bf16_lo(r4[e]), bf16_hi(r4[e]));
-                        float2& a = acc[8 * cc + k / 2];
-                        a = fma2(f2(fy, fy), yy, a);
+                        float2 g = fma2(f2(fy, fy), yy, f2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])));
                         dy = fmaf(yy.x, kk.x, fmaf(yy.y, kk.y, dy));
                         if (krows) {
                             const float2 zz = f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1]));
-                            a = fma2(f2(tail, tail), zz, a);
+                            g = fma2(f2(tail, tail), zz, g);
                             dz = fmaf(zz.x, kk.x, fmaf(zz.y, kk.y, dz));
                         }
+                        a[k] = __float_as_uint(g.x);
+                        a[k + 1] = __float_as_uint(g.y);
+                        o[e] = pack_bf16x2(g.x, g.y);
                     }
+                    if (last) *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
+                if (!last) tmem_st16(lb + TG_ACC + col, a);
             }
+            if (last) fence_proxy_async_smem();
+            else tmem_wait_st();
             tc_fence_before();
             arrive(B_YZF);
+            if (last) arrive(B_DONE);
             rc = fmaf(fy, dy, rc);
             if (krows) {
                 rk = tail * dz;
@@ -437,32 +480,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 rowb[part * C + i] = rb;
             }
             rowc[part * 2 * C + t] = rc;
-            arrive(B_ROWS + (hh & 1));
-        }
-        // dk, dq into the tile of k and q
-        if (ok && wwait(B_ACC, hpg - 1)) {
-            tc_fence_after();
-#pragma unroll
-            for (int cc = 0; cc < HC / 16; ++cc) {
-                const int col = c0 + 16 * cc;
-                uint32_t y[16];
-                tmem_ld16(lb + TG_ACC + col, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int k = 8 * c + 2 * e;
-                        const float2 a = add2(acc[8 * cc + k / 2], f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
-                        o[e] = pack_bf16x2(a.x, a.y);
-                    }
-                    *reinterpret_cast<uint4*>(sm + L::KQ + (col >> 6) * SLAB + tile_off<128>(t, ((col & 63) >> 3) + c)) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            arrive(B_DONE);
+            arrive(B_ROWS + ph);
         }
     }
     tc_fence_before();
@@ -492,7 +510,8 @@ cudaError_t launch_grad(const GDRArgs& a, const CallMaps& m, cudaStream_t s) {
     if ((e = map_steps(&mv, a.v, DV, a.nheads, a.seqlen, a.batch)) != cudaSuccess) return e;
     static std::atomic<uint64_t> attr_done{0};
     if ((e = allow_dynamic_smem(reinterpret_cast<const void*>(gdr_bwd_grad_kernel<DK, DV>), bytes, attr_done)) != cudaSuccess) return e;
-    gdr_bwd_grad_kernel<DK, DV><<<(unsigned)(a.batch * a.ngroups * a.nchunks), GTHREADS, bytes, s>>>(m.k, m.q, mv, m.v, mdk, mdq, a);
+    const int64_t items = a.batch * a.ngroups * a.nchunks;
+    gdr_bwd_grad_kernel<DK, DV><<<(unsigned)(items < 148 ? items : 148), GTHREADS, bytes, s>>>(m.k, m.q, mv, m.v, mdk, mdq, a);
     return cudaGetLastError();
 }
 
