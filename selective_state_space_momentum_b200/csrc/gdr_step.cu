@@ -10,9 +10,12 @@
 // the step: two dot products of a row (with k and with q, the second as
 // o = scale ((e^g S) q + u (k . q)), so that both are formed in one pass over
 // the loaded row and one shuffle reduction serves both).  All arithmetic is
-// fp32.  Eight lanes a row (16 above 128 states) keep 16 states a lane in
-// flight.  Measured: 184 us for 512 requests of 32 heads of 64 x 128 (5.9 TB/s),
-// 3.1 us for one request of 32 heads of 128 x 128.
+// fp32.  Eight lanes a row (16 above 128 states) and 12 blocks an SM keep 96 KB
+// of states in flight.  Measured: 175 us for 512 requests of 32 heads of 64 x 128
+// (6.2 TB/s), 3.2 us for one request of 32 heads of 128 x 128.  With 8 blocks an
+// SM (k kept in registers) 184, with loads and stores that stay in the caches
+// 194; after a flush of dirty lines, against 202 with 12 blocks: 216 with 16
+// (spills), 222 with 8, 242 with 16 lanes a row, 294 with 32, 236 with 4.
 #include "mm_common.cuh"
 #include "mm_internal.h"
 
@@ -22,7 +25,7 @@ namespace {
 
 // LPR lanes hold a row of N <= 4 LPR NV states as NV vectors of four each.
 template <typename IO, int LPR, int NV>
-__global__ void __launch_bounds__(128) gdr_step_kernel(const GDRStepArgs p) {
+__global__ void __launch_bounds__(128, 12) gdr_step_kernel(const GDRStepArgs p) {
     const int lane = threadIdx.x % LPR;
     const int64_t rows = p.batch * p.nheads * p.headdim;
     const int64_t row0 = ((int64_t)blockIdx.x * 128 + threadIdx.x) / LPR;
@@ -36,12 +39,12 @@ __global__ void __launch_bounds__(128) gdr_step_kernel(const GDRStepArgs p) {
     const IO* q = static_cast<const IO*>(p.q) + gk;
     float* S = p.h + row * N;
 
-    float4 s[NV], kk[NV];
+    float4 s[NV];
     float sk = 0.0f, sq = 0.0f, kq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int n = (lane + i * LPR) * 4;
-        s[i] = kk[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (n < N) s[i] = __ldcs(reinterpret_cast<const float4*>(S + n));
     }
     const float a = ex2_approx(load1(static_cast<const IO*>(p.g) + bh) * kLog2e);
@@ -51,12 +54,12 @@ __global__ void __launch_bounds__(128) gdr_step_kernel(const GDRStepArgs p) {
     for (int i = 0; i < NV; ++i) {
         const int n = (lane + i * LPR) * 4;
         if (n >= N) continue;
-        kk[i] = load4(k + n);
+        const float4 kk = load4(k + n);
         const float4 qq = load4(q + n);
         s[i].x *= a; s[i].y *= a; s[i].z *= a; s[i].w *= a;
-        sk = fmaf(s[i].x, kk[i].x, fmaf(s[i].y, kk[i].y, fmaf(s[i].z, kk[i].z, fmaf(s[i].w, kk[i].w, sk))));
+        sk = fmaf(s[i].x, kk.x, fmaf(s[i].y, kk.y, fmaf(s[i].z, kk.z, fmaf(s[i].w, kk.w, sk))));
         sq = fmaf(s[i].x, qq.x, fmaf(s[i].y, qq.y, fmaf(s[i].z, qq.z, fmaf(s[i].w, qq.w, sq))));
-        kq = fmaf(kk[i].x, qq.x, fmaf(kk[i].y, qq.y, fmaf(kk[i].z, qq.z, fmaf(kk[i].w, qq.w, kq))));
+        kq = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, kq))));
     }
 #pragma unroll
     for (int m = LPR / 2; m >= 1; m >>= 1) {
@@ -70,9 +73,10 @@ __global__ void __launch_bounds__(128) gdr_step_kernel(const GDRStepArgs p) {
     for (int i = 0; i < NV; ++i) {
         const int n = (lane + i * LPR) * 4;
         if (n >= N) continue;
+        const float4 kk = load4(k + n);                      // (again, from L1: kept, its registers cost four blocks an SM)
         __stcs(reinterpret_cast<float4*>(S + n),
-               make_float4(fmaf(u, kk[i].x, s[i].x), fmaf(u, kk[i].y, s[i].y), fmaf(u, kk[i].z, s[i].z),
-                           fmaf(u, kk[i].w, s[i].w)));
+               make_float4(fmaf(u, kk.x, s[i].x), fmaf(u, kk.y, s[i].y), fmaf(u, kk.z, s[i].z),
+                           fmaf(u, kk.w, s[i].w)));
     }
     if (lane == 0) store1(static_cast<IO*>(p.o) + row, p.scale * fmaf(u, kq, sq));
 }
