@@ -26,6 +26,7 @@ Convenience wrappers allocate outputs:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -1069,7 +1070,10 @@ def scan_fwd_split_peers(x, delta, A, B, C, seg_len, seqlen_total, peers, h0=Non
 # so these wrappers are written for few Python operations a call: an operand
 # that is as it should be passes four comparisons; any other goes to _require
 # for its message.  Workspace sizes are asked of the library once
-# per set of sizes.
+# per set of sizes.  Outputs and workspaces come from the pool of the stream the
+# call runs on, so a call on another stream needs no ordering behind the current
+# one; its inputs have to be ready on its own stream, and the current stream has
+# to wait for it before it reads what the call returned.
 def _operands(items, device, index):
     """Check (name, tensor, shape, dtype, optional) operands; their pointers."""
     ptrs = []
@@ -1103,15 +1107,40 @@ def _run(index, stream, fn, *args):
         return fn(*args, stream)
 
 
-def _hold(stream, *tensors):
-    """Tensors a wrapper allocated on the current stream and used on another
-    one: the allocator may hand their memory out again only after that
-    stream's work."""
+_HERE = contextlib.nullcontext()
+
+
+def _side(stream, device):
+    """The torch stream behind a wrapper's ``stream`` argument; None where that
+    is the device's current stream."""
     import torch
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+    if stream is None:
+        return None
+    _on_cuda(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return None if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream else stream
+
+
+def _pool(side):
+    """Where a wrapper allocates what its kernels touch: from the pool of the
+    stream they run on.  A block that the current stream's pool hands out may
+    have been freed there a moment ago, with work that uses it still queued,
+    and nothing orders another stream behind that work."""
+    import torch
+    return _HERE if side is None else torch.cuda.stream(side)
+
+
+def _give(side, device, *tensors):
+    """Tensors from another stream's pool that a wrapper returns: the caller
+    goes on with them on the current stream, so their memory may be handed out
+    again only after that stream's work too."""
+    import torch
+    if side is not None:
+        current = torch.cuda.current_stream(device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(current)
 
 
 def _require_bytes(name, t, nbytes, index):
@@ -1249,12 +1278,13 @@ def gdr_fwd(q, k, v, g, beta, h0=None, scale=None, return_last_state=True, strea
     import torch
     sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
     dev = v.device
-    o = torch.empty_like(v)
-    hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
-    ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, False), device=dev, dtype=torch.uint8)
+    side = _side(stream, dev)
+    with _pool(side):
+        o = torch.empty_like(v)
+        hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
+        ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, False), device=dev, dtype=torch.uint8)
     _gdr_fwd(sizes, q, k, v, g, beta, h0, N ** -0.5 if scale is None else scale, o, hT, None, ws, stream)
-    if stream is not None:
-        _hold(stream, o, hT, ws)
+    _give(side, dev, o, hT)
     return o, hT
 
 
@@ -1264,13 +1294,14 @@ def gdr_fwd_train(q, k, v, g, beta, h0=None, scale=None, return_last_state=False
     import torch
     sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
     dev = v.device
-    o = torch.empty_like(v)
-    hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
-    ckpt = torch.empty(mm_gdr_ckpt_size(*sizes), device=dev, dtype=torch.uint8)
-    ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, True), device=dev, dtype=torch.uint8)
+    side = _side(stream, dev)
+    with _pool(side):
+        o = torch.empty_like(v)
+        hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
+        ckpt = torch.empty(mm_gdr_ckpt_size(*sizes), device=dev, dtype=torch.uint8)
+        ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, True), device=dev, dtype=torch.uint8)
     _gdr_fwd(sizes, q, k, v, g, beta, h0, N ** -0.5 if scale is None else scale, o, hT, ckpt, ws, stream)
-    if stream is not None:
-        _hold(stream, o, hT, ckpt, ws)
+    _give(side, dev, o, hT, ckpt)
     return o, hT, ckpt
 
 
@@ -1279,16 +1310,18 @@ def gdr_bwd(q, k, v, g, beta, ckpt, dout, dhT=None, scale=None, return_dh0=False
     dv, dg, dbeta and, with ``return_dh0``, dh0."""
     import torch
     sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
-    grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
-             "dg": torch.empty((B, L, H), device=v.device, dtype=v.dtype),
-             "dbeta": torch.empty((B, L, H), device=v.device, dtype=v.dtype)}
-    dh0 = torch.empty((B, H, P, N), device=v.device, dtype=torch.float32) if return_dh0 else None
-    ws = torch.empty(mm_gdr_bwd_workspace_size(*sizes), device=v.device, dtype=torch.uint8)
+    dev = v.device
+    side = _side(stream, dev)
+    with _pool(side):
+        grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
+                 "dg": torch.empty((B, L, H), device=dev, dtype=v.dtype),
+                 "dbeta": torch.empty((B, L, H), device=dev, dtype=v.dtype)}
+        dh0 = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_dh0 else None
+        ws = torch.empty(mm_gdr_bwd_workspace_size(*sizes), device=dev, dtype=torch.uint8)
     _gdr_bwd(sizes, q, k, v, g, beta, N ** -0.5 if scale is None else scale, ckpt, dout, dhT, *grads.values(), dh0, ws, stream)
     if return_dh0:
         grads["dh0"] = dh0
-    if stream is not None:
-        _hold(stream, ws, *grads.values())
+    _give(side, dev, *grads.values())
     return grads
 
 
@@ -1297,10 +1330,11 @@ def gdr_step(q, k, v, g, beta, h, scale=None, stream=None):
     updated in place; returns o (batch, H, P)."""
     import torch
     sizes = _gdr_sizes(q, v, 3)
-    o = torch.empty_like(v)
+    side = _side(stream, v.device)
+    with _pool(side):
+        o = torch.empty_like(v)
     _gdr_step(sizes, q, k, v, g, beta, h, sizes[4] ** -0.5 if scale is None else scale, o, stream)
-    if stream is not None:
-        _hold(stream, o)
+    _give(side, v.device, o)
     return o
 
 
@@ -1374,12 +1408,13 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
     by silu(z) when z is given: returns (y, mean, rstd), mean None with rms."""
     import torch
     sizes = _norm_dims(x)
-    y = torch.empty_like(x)
-    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    mean = None if rms else torch.empty_like(rstd)
+    side = _side(stream, x.device)
+    with _pool(side):
+        y = torch.empty_like(x)
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        mean = None if rms else torch.empty_like(rstd)
     _norm_fwd(sizes, x, weight, bias, z, eps, rms, y, mean, rstd, stream)
-    if stream is not None:
-        _hold(stream, y, mean, rstd)
+    _give(side, x.device, y, mean, rstd)
     return y, mean, rstd
 
 
@@ -1388,17 +1423,19 @@ def layer_norm_bwd(x, weight, bias, mean, rstd, dy, z=None, rms=False, stream=No
     dx and, for each that was given, dweight, dbias, dz."""
     import torch
     sizes = rows, cols = _norm_dims(x)
-    grads = {"dx": torch.empty_like(x)}
-    ws = None
-    if weight is not None or bias is not None:
-        ws = torch.empty(mm_layer_norm_bwd_workspace_size(rows, cols, _io_code(x.dtype)), device=x.device, dtype=torch.uint8)
-        for name, t in (("dweight", weight), ("dbias", bias)):
-            if t is not None:
-                grads[name] = torch.empty((cols,), device=x.device, dtype=torch.float32)
-    if z is not None:
-        grads["dz"] = torch.empty_like(x)
+    dev = x.device
+    side = _side(stream, dev)
+    with _pool(side):
+        grads = {"dx": torch.empty_like(x)}
+        ws = None
+        if weight is not None or bias is not None:
+            ws = torch.empty(mm_layer_norm_bwd_workspace_size(rows, cols, _io_code(x.dtype)), device=dev, dtype=torch.uint8)
+            for name, t in (("dweight", weight), ("dbias", bias)):
+                if t is not None:
+                    grads[name] = torch.empty((cols,), device=dev, dtype=torch.float32)
+        if z is not None:
+            grads["dz"] = torch.empty_like(x)
     _norm_bwd(sizes, x, weight, bias, z, rms, mean, rstd, dy, grads["dx"], grads.get("dweight"), grads.get("dbias"),
               grads.get("dz"), ws, stream)
-    if stream is not None:
-        _hold(stream, ws, *grads.values())
+    _give(side, dev, *grads.values())
     return grads

@@ -1,0 +1,135 @@
+"""On which stream the allocating wrappers take their memory (no GPU).
+
+A block that was freed on a stream goes back to that stream's pool at once: the
+work queued there before it may still be using it.  So what a wrapper's kernels
+touch on ``stream`` has to come from the pool of ``stream``, not from that of
+the caller's current stream, which ``stream`` is not ordered behind; and what
+the wrapper returns has to be recorded for the current stream, on which the
+caller goes on with it.  Streams, allocations and launches are stood in for
+here; the tensors are host tensors.
+"""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import selective_state_space_momentum_b200 as mm  # noqa: E402
+
+HERE = torch.device("cpu")
+
+
+class _Stream:
+    def __init__(self, handle, device=HERE):
+        self.cuda_stream, self.device = handle, device
+
+    def wait_stream(self, other):
+        pass
+
+
+class _Lib:
+    """The library with its launches counted and not made."""
+
+    def __init__(self, real, log):
+        self._real, self._log = real, log
+
+    def __getattr__(self, name):
+        if name.endswith("_size") or name == "mm_last_error":
+            return getattr(self._real, name)
+
+        def launch(*args):
+            handle = args[-1]
+            self._log.append((name, getattr(handle, "value", handle) or 0))
+            return 0
+        return launch
+
+
+@pytest.fixture
+def stage(monkeypatch):
+    """current: the caller's stream; made: storage -> stream it was allocated on; recorded: (storage, handle)."""
+    class Stage:
+        pass
+    st = Stage()
+    st.current, st.default = _Stream(11), _Stream(0)
+    st.made, st.recorded, st.launched, st.external, st.alive = {}, set(), [], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, st.current = st.current, stream
+        yield
+        st.current = before
+
+    def external(handle, device=None):
+        st.external.append((handle, device))
+        return _Stream(handle, HERE if device is None else torch.device(device))
+
+    def recording(fn):
+        def make(*args, **kwargs):
+            kwargs.pop("device", None)
+            t = fn(*args, **kwargs)
+            st.made[t.data_ptr()] = st.current.cuda_stream
+            st.alive.append(t)
+            return t
+        return make
+    real = mm.load_library()
+    lib = _Lib(real, st.launched)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: st.current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: st.default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch, "empty", recording(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", recording(torch.empty_like))
+    monkeypatch.setattr(torch.Tensor, "new_empty", recording(torch.Tensor.new_empty))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: st.recorded.add((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(mm, "_on_cuda", lambda device: None)
+    monkeypatch.setattr(mm, "load_library", lambda path=None: lib)
+    monkeypatch.setattr(mm, "_run", lambda index, stream, fn, *args: fn(*args, stream if isinstance(stream, int) else
+                                                                        (stream or st.current).cuda_stream))
+    return st
+
+
+def _gdr(ndim=4):
+    lead = (2, 70) if ndim == 4 else (2,)
+    z = lambda *s: torch.zeros(*lead, *s, dtype=torch.bfloat16)
+    return [z(2, 64), z(2, 64), z(4, 64), z(4), z(4)]
+
+
+def _ckpt():
+    return torch.zeros(mm.mm_gdr_ckpt_size(2, 70, 4, 64, 64, 2), dtype=torch.uint8)
+
+
+X = torch.zeros(6, 40)
+NEW = {
+    "gdr_fwd": lambda s: mm.gdr_fwd(*_gdr(), stream=s),
+    "gdr_fwd_train": lambda s: mm.gdr_fwd_train(*_gdr(), return_last_state=True, stream=s),
+    "gdr_bwd": lambda s: mm.gdr_bwd(*_gdr(), _ckpt(), _gdr()[2], return_dh0=True, stream=s),
+    "gdr_step": lambda s: mm.gdr_step(*_gdr(3), torch.zeros(2, 4, 64, 64), stream=s),
+    "layer_norm_fwd": lambda s: mm.layer_norm_fwd(X, stream=s),
+    "layer_norm_bwd": lambda s: mm.layer_norm_bwd(X, torch.zeros(40), torch.zeros(40), torch.zeros(6), torch.zeros(6), X, z=X, stream=s),
+}
+
+
+def _tensors(out):
+    values = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else [out]
+    return [t for t in values if t is not None]
+
+
+def _check(st, call, stream, handle):
+    out = _tensors(call(stream))
+    assert st.made and set(st.made.values()) == {handle}, st.made
+    assert st.launched and {h for _, h in st.launched} == {handle}
+    assert out
+    for t in out:
+        recorded = (t.data_ptr(), st.current.cuda_stream) in st.recorded
+        assert recorded == (handle != st.current.cuda_stream)
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_memory_belongs_to_the_stream_that_uses_it(stage, name):
+    _check(stage, NEW[name], _Stream(77), 77)
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_current_stream_by_default_and_by_name(stage, name):
+    _check(stage, NEW[name], None, 11)
+    _check(stage, NEW[name], stage.current, 11)
