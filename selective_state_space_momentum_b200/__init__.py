@@ -1111,14 +1111,17 @@ _HERE = contextlib.nullcontext()
 
 
 def _side(stream, device):
-    """The torch stream behind a wrapper's ``stream`` argument; None where that
-    is the device's current stream."""
+    """The torch stream behind a wrapper's ``stream`` argument (an integer: a
+    stream of the operands' device, 0 its default one); None where that is the
+    device's current stream."""
     import torch
     if stream is None:
         return None
     _on_cuda(device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+    if isinstance(stream, int):                              # (torch takes a handle of 0 for "none given")
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
     return None if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream else stream
 
 

@@ -133,3 +133,20 @@ def test_memory_belongs_to_the_stream_that_uses_it(stage, name):
 def test_current_stream_by_default_and_by_name(stage, name):
     _check(stage, NEW[name], None, 11)
     _check(stage, NEW[name], stage.current, 11)
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_stream_handles(stage, name):
+    """An integer handle: a stream of the operands' device; 0 is the default stream."""
+    _check(stage, NEW[name], 77, 77)
+    assert set(stage.external) == {(77, HERE)}
+    stage.made.clear(), stage.launched.clear(), stage.external.clear()
+    _check(stage, NEW[name], 0, 0)
+    assert stage.external == []
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_a_stream_of_another_device_is_refused(stage, name):
+    with pytest.raises(ValueError, match="stream"):
+        NEW[name](_Stream(77, torch.device("meta")))
+    assert stage.launched == []
