@@ -685,6 +685,50 @@ def mm_device_status():
 
 
 # ------------------------------------------------------------ wrappers -----
+# The wrappers below allocate what they return (and workspaces) from the pool of
+# the stream the call runs on, so a call on another stream needs no ordering
+# behind the current one; its inputs have to be ready on its own stream, and the
+# current stream has to wait for it before it reads what the call returned.
+_HERE = contextlib.nullcontext()
+
+
+def _side(stream, like):
+    """The torch stream behind a wrapper's ``stream`` argument (an integer: a
+    stream of the device that holds `like`, 0 its default one); None where that
+    is the device's current stream."""
+    import torch
+    if stream is None:
+        return None
+    device = like.device
+    _on_cuda(device)
+    if isinstance(stream, int):                              # (torch takes a handle of 0 for "none given")
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+    return None if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream else stream
+
+
+def _pool(side):
+    """Where a wrapper allocates what its kernels touch: from the pool of the
+    stream they run on.  A block that the current stream's pool hands out may
+    have been freed there a moment ago, with work that uses it still queued,
+    and nothing orders another stream behind that work."""
+    import torch
+    return _HERE if side is None else torch.cuda.stream(side)
+
+
+def _give(side, *tensors):
+    """Tensors from another stream's pool that a wrapper returns: the caller
+    goes on with them on the current stream, so their memory may be handed out
+    again only after that stream's work too."""
+    import torch
+    if side is not None:
+        current = torch.cuda.current_stream(side.device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(current)
+
+
 def scan_fwd(x, delta, A, B, C, h0=None, v0=None, beta=0.9, alpha=1.0,
              return_last_state=True, stream=None, D=None, z=None, delta_bias=None,
              delta_softplus=False):
@@ -692,17 +736,20 @@ def scan_fwd(x, delta, A, B, C, h0=None, v0=None, beta=0.9, alpha=1.0,
     D, z, delta_bias, delta_softplus is given; returns (y, hT, vT) (states
     None when ``return_last_state`` is False)."""
     import torch
-    y = torch.empty_like(x)
+    side = _side(stream, x)
     hT = vT = None
-    if return_last_state:
-        shape = (x.shape[0], x.shape[1], A.shape[1])
-        hT = torch.empty(shape, device=x.device, dtype=torch.float32)
-        vT = torch.empty(shape, device=x.device, dtype=torch.float32)
+    with _pool(side):
+        y = torch.empty_like(x)
+        if return_last_state:
+            shape = (x.shape[0], x.shape[1], A.shape[1])
+            hT = torch.empty(shape, device=x.device, dtype=torch.float32)
+            vT = torch.empty(shape, device=x.device, dtype=torch.float32)
     if D is None and z is None and delta_bias is None and not delta_softplus:
         mm_scan_fwd(x, delta, A, B, C, h0, v0, beta, alpha, y, hT, vT, stream)
     else:
         mm_scan_fwd_gated(x, delta, A, B, C, D, z, delta_bias, delta_softplus, h0, v0, beta, alpha,
                           y, hT, vT, None, stream)
+    _give(side, y, hT, vT)
     return y, hT, vT
 
 
@@ -760,13 +807,16 @@ def scan_fwd_train(x, delta, A, B, C, h0=None, v0=None, beta=0.9, alpha=1.0, str
     import torch
     batch, dim, L = x.shape
     N = A.shape[1]
-    y = torch.empty_like(x)
-    hT = torch.empty((batch, dim, N), device=x.device, dtype=torch.float32)
-    vT = torch.empty_like(hT)
-    ckpt = torch.empty((batch, dim, (L + MM_SCAN_CKPT_STEPS - 1) // MM_SCAN_CKPT_STEPS, 2, N), device=x.device,
-                       dtype=torch.float32)
+    side = _side(stream, x)
+    with _pool(side):
+        y = torch.empty_like(x)
+        hT = torch.empty((batch, dim, N), device=x.device, dtype=torch.float32)
+        vT = torch.empty_like(hT)
+        ckpt = torch.empty((batch, dim, (L + MM_SCAN_CKPT_STEPS - 1) // MM_SCAN_CKPT_STEPS, 2, N), device=x.device,
+                           dtype=torch.float32)
     mm_scan_fwd_gated(x, delta, A, B, C, D, z, delta_bias, delta_softplus, h0, v0, beta, alpha, y, hT, vT,
                       ckpt, stream)
+    _give(side, y, hT, vT, ckpt)
     return y, hT, vT, ckpt
 
 
@@ -779,19 +829,24 @@ def scan_bwd(x, delta, A, B, C, ckpt, dy, h0=None, v0=None, dhT=None, dvT=None, 
     batch, dim, L = x.shape
     N = A.shape[1]
     f32 = dict(device=x.device, dtype=torch.float32)
-    g = {"dx": torch.empty_like(x), "ddelta": torch.empty_like(x), "dA": torch.empty((dim, N), **f32),
-         "dB": torch.empty((batch, N, L), **f32), "dC": torch.empty((batch, N, L), **f32),
-         "dh0": torch.empty((batch, dim, N), **f32), "dv0": torch.empty((batch, dim, N), **f32)}
-    if D is None and z is None and delta_bias is None and not delta_softplus:
+    plain = D is None and z is None and delta_bias is None and not delta_softplus
+    side = _side(stream, x)
+    with _pool(side):
+        g = {"dx": torch.empty_like(x), "ddelta": torch.empty_like(x), "dA": torch.empty((dim, N), **f32),
+             "dB": torch.empty((batch, N, L), **f32), "dC": torch.empty((batch, N, L), **f32),
+             "dh0": torch.empty((batch, dim, N), **f32), "dv0": torch.empty((batch, dim, N), **f32)}
+        if not plain:
+            g["dD"] = torch.empty((dim,), **f32)
+            g["ddelta_bias"] = torch.empty((dim,), **f32)
+            g["dz"] = torch.empty_like(x) if z is not None else None
+    if plain:
         mm_scan_bwd(x, delta, A, B, C, h0, v0, beta, alpha, ckpt, dy, dhT, dvT, g["dx"], g["ddelta"],
                     g["dA"], g["dB"], g["dC"], g["dh0"], g["dv0"], stream)
-        return g
-    g["dD"] = torch.empty((dim,), **f32)
-    g["ddelta_bias"] = torch.empty((dim,), **f32)
-    g["dz"] = torch.empty_like(x) if z is not None else None
-    mm_scan_bwd_gated(x, delta, A, B, C, D, z, delta_bias, delta_softplus, h0, v0, beta, alpha, ckpt, dy,
-                      dhT, dvT, g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"],
-                      g["ddelta_bias"], g["dh0"], g["dv0"], stream)
+    else:
+        mm_scan_bwd_gated(x, delta, A, B, C, D, z, delta_bias, delta_softplus, h0, v0, beta, alpha, ckpt, dy,
+                          dhT, dvT, g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"],
+                          g["ddelta_bias"], g["dh0"], g["dv0"], stream)
+    _give(side, *g.values())
     return g
 
 
@@ -800,9 +855,12 @@ def ssd_fwd(x, delta, A, B, C, h0=None, alpha=1.0, chunk=256, return_last_state=
     import torch
     batch, L, H, P = x.shape
     N = B.shape[3]
-    y = torch.empty_like(x)
-    hT = torch.empty((batch, H, P, N), device=x.device, dtype=torch.float32) if return_last_state else None
+    side = _side(stream, x)
+    with _pool(side):
+        y = torch.empty_like(x)
+        hT = torch.empty((batch, H, P, N), device=x.device, dtype=torch.float32) if return_last_state else None
     mm_ssd_fwd(x, delta, A, B, C, h0, 0.0, alpha, y, hT, chunk, stream)
+    _give(side, y, hT)
     return y, hT
 
 
@@ -811,10 +869,13 @@ def ssd_fwd_momentum(x, delta, A, B, C, h0=None, v0=None, beta=0.9, alpha=1.0, s
     import torch
     batch, L, H, P = x.shape
     N = B.shape[3]
-    y = torch.empty_like(x)
-    hT = torch.empty((batch, H, P, N), device=x.device, dtype=torch.float32)
-    vT = torch.empty_like(hT)
+    side = _side(stream, x)
+    with _pool(side):
+        y = torch.empty_like(x)
+        hT = torch.empty((batch, H, P, N), device=x.device, dtype=torch.float32)
+        vT = torch.empty_like(hT)
     mm_ssd_fwd_momentum(x, delta, A, B, C, h0, v0, beta, alpha, y, hT, vT, stream)
+    _give(side, y, hT, vT)
     return y, hT, vT
 
 
@@ -953,22 +1014,26 @@ def scan_fwd_split(x, delta, A, B, C, seg_len, seqlen_total, h0=None, v0=None, b
     per = split_pieces(int(seqlen_total), world, int(seg_len))[0][1] // int(seg_len) if world > 1 else \
         -(-steps // int(seg_len))
     rec = mm_scan_split_maps_size(batch, steps, dim, N, 1, io)
-    local = torch.empty(per * rec, dtype=torch.uint8, device=x.device)
-    y = torch.empty_like(x)
+    side = _side(stream, x)
+    with _pool(side):
+        local = torch.empty(per * rec, dtype=torch.uint8, device=x.device)
+        y = torch.empty_like(x)
+        hT = torch.empty((batch, dim, N), device=x.device, dtype=torch.float32)
+        vT = torch.empty_like(hT)
     mm_scan_fwd_split_maps(x, delta, A, B, C, beta, alpha, y, local, seg_len, stream)
     if world > 1:
         # the collective runs on torch's current stream: order it after the launch
-        if stream is not None:
-            torch.cuda.current_stream(x.device).wait_stream(stream)
+        if side is not None:
+            torch.cuda.current_stream(x.device).wait_stream(side)
         gathered = _all_gather_bytes(local, world, group)
-        if stream is not None:
-            stream.wait_stream(torch.cuda.current_stream(x.device))
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream(x.device))
+            gathered.record_stream(side)                     # from the current stream's pool, read on the other
     else:
         gathered = local
-    hT = torch.empty((batch, dim, N), device=x.device, dtype=torch.float32)
-    vT = torch.empty_like(hT)
     mm_scan_fwd_split_correct(delta, A, C, h0, v0, beta, alpha, y, hT, vT, gathered, seg_len, first,
                               seqlen_total, stream)
+    _give(side, local, y, hT, vT)
     return y, hT, vT
 
 
@@ -1054,14 +1119,17 @@ def scan_fwd_split_peers(x, delta, A, B, C, seg_len, seqlen_total, peers, h0=Non
         raise ValueError(f"rank {peers.rank} holds steps [{first}, {first + steps}): x must be (batch, dim, {steps})")
     batch, dim, _ = x.shape
     N = A.shape[1]
-    y = torch.empty_like(x)
+    side = _side(stream, x)
+    with _pool(side):
+        y = torch.empty_like(x)
+        hT = torch.empty((batch, dim, N), device=x.device, dtype=torch.float32)
+        vT = torch.empty_like(hT)
     dests, local = peers.next()
     mm_scan_fwd_split_maps_peers(x, delta, A, B, C, beta, alpha, y, dests, seg_len, first, seqlen_total, stream)
-    peers.barrier(stream)
-    hT = torch.empty((batch, dim, N), device=x.device, dtype=torch.float32)
-    vT = torch.empty_like(hT)
+    peers.barrier(side)
     mm_scan_fwd_split_correct(delta, A, C, h0, v0, beta, alpha, y, hT, vT, local, seg_len, first,
                               seqlen_total, stream)
+    _give(side, y, hT, vT)
     return y, hT, vT
 
 
@@ -1070,10 +1138,7 @@ def scan_fwd_split_peers(x, delta, A, B, C, seg_len, seqlen_total, peers, h0=Non
 # so these wrappers are written for few Python operations a call: an operand
 # that is as it should be passes four comparisons; any other goes to _require
 # for its message.  Workspace sizes are asked of the library once
-# per set of sizes.  Outputs and workspaces come from the pool of the stream the
-# call runs on, so a call on another stream needs no ordering behind the current
-# one; its inputs have to be ready on its own stream, and the current stream has
-# to wait for it before it reads what the call returned.
+# per set of sizes.
 def _operands(items, device, index):
     """Check (name, tensor, shape, dtype, optional) operands; their pointers."""
     ptrs = []
@@ -1105,45 +1170,6 @@ def _run(index, stream, fn, *args):
         return fn(*args, stream)
     with torch.cuda.device(index):
         return fn(*args, stream)
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _side(stream, device):
-    """The torch stream behind a wrapper's ``stream`` argument (an integer: a
-    stream of the operands' device, 0 its default one); None where that is the
-    device's current stream."""
-    import torch
-    if stream is None:
-        return None
-    _on_cuda(device)
-    if isinstance(stream, int):                              # (torch takes a handle of 0 for "none given")
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
-    return None if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream else stream
-
-
-def _pool(side):
-    """Where a wrapper allocates what its kernels touch: from the pool of the
-    stream they run on.  A block that the current stream's pool hands out may
-    have been freed there a moment ago, with work that uses it still queued,
-    and nothing orders another stream behind that work."""
-    import torch
-    return _HERE if side is None else torch.cuda.stream(side)
-
-
-def _give(side, device, *tensors):
-    """Tensors from another stream's pool that a wrapper returns: the caller
-    goes on with them on the current stream, so their memory may be handed out
-    again only after that stream's work too."""
-    import torch
-    if side is not None:
-        current = torch.cuda.current_stream(device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(current)
 
 
 def _require_bytes(name, t, nbytes, index):
@@ -1281,13 +1307,13 @@ def gdr_fwd(q, k, v, g, beta, h0=None, scale=None, return_last_state=True, strea
     import torch
     sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
     dev = v.device
-    side = _side(stream, dev)
+    side = _side(stream, v)
     with _pool(side):
         o = torch.empty_like(v)
         hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
         ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, False), device=dev, dtype=torch.uint8)
     _gdr_fwd(sizes, q, k, v, g, beta, h0, N ** -0.5 if scale is None else scale, o, hT, None, ws, stream)
-    _give(side, dev, o, hT)
+    _give(side, o, hT)
     return o, hT
 
 
@@ -1297,14 +1323,14 @@ def gdr_fwd_train(q, k, v, g, beta, h0=None, scale=None, return_last_state=False
     import torch
     sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
     dev = v.device
-    side = _side(stream, dev)
+    side = _side(stream, v)
     with _pool(side):
         o = torch.empty_like(v)
         hT = torch.empty((B, H, P, N), device=dev, dtype=torch.float32) if return_last_state else None
         ckpt = torch.empty(mm_gdr_ckpt_size(*sizes), device=dev, dtype=torch.uint8)
         ws = torch.empty(mm_gdr_fwd_workspace_size(*sizes, True), device=dev, dtype=torch.uint8)
     _gdr_fwd(sizes, q, k, v, g, beta, h0, N ** -0.5 if scale is None else scale, o, hT, ckpt, ws, stream)
-    _give(side, dev, o, hT, ckpt)
+    _give(side, o, hT, ckpt)
     return o, hT, ckpt
 
 
@@ -1314,7 +1340,7 @@ def gdr_bwd(q, k, v, g, beta, ckpt, dout, dhT=None, scale=None, return_dh0=False
     import torch
     sizes = B, L, H, P, N, G = _gdr_sizes(q, v)
     dev = v.device
-    side = _side(stream, dev)
+    side = _side(stream, v)
     with _pool(side):
         grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
                  "dg": torch.empty((B, L, H), device=dev, dtype=v.dtype),
@@ -1324,7 +1350,7 @@ def gdr_bwd(q, k, v, g, beta, ckpt, dout, dhT=None, scale=None, return_dh0=False
     _gdr_bwd(sizes, q, k, v, g, beta, N ** -0.5 if scale is None else scale, ckpt, dout, dhT, *grads.values(), dh0, ws, stream)
     if return_dh0:
         grads["dh0"] = dh0
-    _give(side, dev, *grads.values())
+    _give(side, *grads.values())
     return grads
 
 
@@ -1333,11 +1359,11 @@ def gdr_step(q, k, v, g, beta, h, scale=None, stream=None):
     updated in place; returns o (batch, H, P)."""
     import torch
     sizes = _gdr_sizes(q, v, 3)
-    side = _side(stream, v.device)
+    side = _side(stream, v)
     with _pool(side):
         o = torch.empty_like(v)
     _gdr_step(sizes, q, k, v, g, beta, h, sizes[4] ** -0.5 if scale is None else scale, o, stream)
-    _give(side, v.device, o)
+    _give(side, o)
     return o
 
 
@@ -1411,13 +1437,13 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, rms=False, strea
     by silu(z) when z is given: returns (y, mean, rstd), mean None with rms."""
     import torch
     sizes = _norm_dims(x)
-    side = _side(stream, x.device)
+    side = _side(stream, x)
     with _pool(side):
         y = torch.empty_like(x)
         rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
         mean = None if rms else torch.empty_like(rstd)
     _norm_fwd(sizes, x, weight, bias, z, eps, rms, y, mean, rstd, stream)
-    _give(side, x.device, y, mean, rstd)
+    _give(side, y, mean, rstd)
     return y, mean, rstd
 
 
@@ -1427,7 +1453,7 @@ def layer_norm_bwd(x, weight, bias, mean, rstd, dy, z=None, rms=False, stream=No
     import torch
     sizes = rows, cols = _norm_dims(x)
     dev = x.device
-    side = _side(stream, dev)
+    side = _side(stream, x)
     with _pool(side):
         grads = {"dx": torch.empty_like(x)}
         ws = None
@@ -1440,5 +1466,5 @@ def layer_norm_bwd(x, weight, bias, mean, rstd, dy, z=None, rms=False, stream=No
             grads["dz"] = torch.empty_like(x)
     _norm_bwd(sizes, x, weight, bias, z, rms, mean, rstd, dy, grads["dx"], grads.get("dweight"), grads.get("dbias"),
               grads.get("dz"), ws, stream)
-    _give(side, dev, *grads.values())
+    _give(side, *grads.values())
     return grads

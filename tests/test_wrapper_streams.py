@@ -109,6 +109,42 @@ NEW = {
 }
 
 
+def _scan():
+    x = torch.zeros(2, 8, 64)
+    bc = torch.zeros(2, 16, 64)
+    return [x, x, torch.zeros(8, 16), bc, bc]
+
+
+def _ssd():
+    x, bc = torch.zeros(1, 256, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 256, 1, 128, dtype=torch.bfloat16)
+    return [x, torch.zeros(1, 256, 2), torch.zeros(2), bc, bc]
+
+
+class _Peers:
+    """One rank's record buffers, without the device."""
+    rank, world = 0, 1
+
+    def next(self):
+        return torch.zeros(1, dtype=torch.int64), torch.zeros(mm.mm_scan_split_maps_size(2, 64, 8, 16, 2), dtype=torch.uint8)
+
+    def barrier(self, stream=None):
+        assert stream is None or stream.cuda_stream in (77, 0)
+
+
+SCAN_CKPT = torch.zeros(2, 8, 4, 2, 16)
+EARLIER = {
+    "scan_fwd": lambda s: mm.scan_fwd(*_scan(), stream=s),
+    "scan_fwd_gated": lambda s: mm.scan_fwd(*_scan(), stream=s, D=torch.zeros(8), z=_scan()[0]),
+    "scan_fwd_train": lambda s: mm.scan_fwd_train(*_scan(), stream=s),
+    "scan_bwd": lambda s: mm.scan_bwd(*_scan(), SCAN_CKPT, _scan()[0], stream=s),
+    "scan_bwd_gated": lambda s: mm.scan_bwd(*_scan(), SCAN_CKPT, _scan()[0], stream=s, D=torch.zeros(8), z=_scan()[0]),
+    "ssd_fwd": lambda s: mm.ssd_fwd(*_ssd(), stream=s),
+    "ssd_fwd_momentum": lambda s: mm.ssd_fwd_momentum(*_ssd(), stream=s),
+    "scan_fwd_split": lambda s: mm.scan_fwd_split(*_scan(), 32, 64, stream=s),
+    "scan_fwd_split_peers": lambda s: mm.scan_fwd_split_peers(*_scan(), 32, 64, _Peers(), stream=s),
+}
+
+
 def _tensors(out):
     values = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else [out]
     return [t for t in values if t is not None]
@@ -150,3 +186,31 @@ def test_a_stream_of_another_device_is_refused(stage, name):
     with pytest.raises(ValueError, match="stream"):
         NEW[name](_Stream(77, torch.device("meta")))
     assert stage.launched == []
+
+
+@pytest.mark.parametrize("name", EARLIER)
+def test_earlier_wrappers(stage, name):
+    _check(stage, EARLIER[name], _Stream(77), 77)
+    stage.made.clear(), stage.launched.clear()
+    _check(stage, EARLIER[name], None, 11)
+    stage.made.clear(), stage.launched.clear()
+    _check(stage, EARLIER[name], 0, 0)
+
+
+def test_split_over_ranks_orders_the_collective(stage, monkeypatch):
+    """The gathered records come from the current stream's pool and are read on the call's."""
+    order = []
+    monkeypatch.setattr(_Stream, "wait_stream", lambda self, other: order.append((self.cuda_stream, other.cuda_stream)))
+    monkeypatch.setattr(torch.distributed, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.distributed, "get_rank", lambda group=None: 0)
+    monkeypatch.setattr(torch.distributed, "get_world_size", lambda group=None: 2)
+    gathered = []
+
+    def gather(local, world, group):
+        order.append("gather")
+        gathered.append(torch.cat([local, local]))
+        return gathered[0]
+    monkeypatch.setattr(mm, "_all_gather_bytes", gather)
+    mm.scan_fwd_split(*_scan(), 32, 128, stream=_Stream(77))
+    assert order == [(11, 77), "gather", (77, 11)]
+    assert (gathered[0].data_ptr(), 77) in stage.recorded and set(stage.made.values()) == {77}

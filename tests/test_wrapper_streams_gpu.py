@@ -61,7 +61,45 @@ def _layer_norm_bwd():
     return lambda s: mm.layer_norm_bwd(x, w, b, mean, rstd, dy, z=z, stream=s)
 
 
-CALLS = {f.__name__[1:]: f for f in (_gdr_fwd, _gdr_fwd_train, _gdr_bwd, _gdr_step, _layer_norm_fwd, _layer_norm_bwd)}
+def _scan_args():
+    gen = torch.Generator().manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()
+    return [r(2, 64, 200), r(2, 64, 200).abs() * 0.1, -r(64, 16).abs(), r(2, 16, 200), r(2, 16, 200)]
+
+
+def _scan_fwd():
+    a = _scan_args()
+    return lambda s: mm.scan_fwd(*a, stream=s)
+
+
+def _scan_fwd_train():
+    a = _scan_args()
+    return lambda s: mm.scan_fwd_train(*a, stream=s)
+
+
+def _scan_fwd_split():
+    a = _scan_args()
+    return lambda s: mm.scan_fwd_split(*a, 64, 200, stream=s)
+
+
+def _ssd(fn, **kw):
+    gen = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()
+    x, B, C = (r(1, 512, n, w).to(torch.bfloat16) for n, w in ((2, 64), (1, 128), (1, 128)))
+    delta, A = r(1, 512, 2).abs() * 0.1, -r(2).abs()
+    return lambda s: fn(x, delta, A, B, C, stream=s, **kw)
+
+
+def _ssd_fwd():
+    return _ssd(mm.ssd_fwd)
+
+
+def _ssd_fwd_momentum():
+    return _ssd(mm.ssd_fwd_momentum)
+
+
+CALLS = {f.__name__[1:]: f for f in (_gdr_fwd, _gdr_fwd_train, _gdr_bwd, _gdr_step, _layer_norm_fwd, _layer_norm_bwd,
+                                     _scan_fwd, _scan_fwd_train, _scan_fwd_split, _ssd_fwd, _ssd_fwd_momentum)}
 
 
 def _values(out):
