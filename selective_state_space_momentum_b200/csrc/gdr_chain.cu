@@ -30,8 +30,10 @@
 // copies of tiles: a thread's own columns of a row would be 32 lines to a store
 // instruction, and the queue behind it is the one the chain's shared-memory
 // accesses wait in.  Every wait is an mbarrier wait bounded by kWaitLimitNs; on
-// give-up the kernel records the fact, every role leaves its loop, waits for
-// its own copies, TMEM is freed and the kernel returns.
+// give-up the kernel records the fact and every role leaves its loop.  Before
+// the CTA frees TMEM and returns, given up or not, the loads' warp has waited
+// for the loads it issued, the products' warp for its products (each with the
+// same limit again) and the stores' warp for its stores.
 //
 // Bound: the latency of the chain -- three products and three passes TMEM ->
 // registers -> shared memory a chunk -- not tensor rate or bytes.  Measured, a
@@ -53,7 +55,7 @@ namespace {
 constexpr int SLAB = 128 * 128;            // 64 columns of the stacked [k; q] tile
 constexpr int EPI_WARPS = 8, NTHREADS = 32 * EPI_WARPS + 96, W_PROD = EPI_WARPS, W_MMA = W_PROD + 1, W_STORE = W_PROD + 2;
 constexpr uint32_t TM_S = 0, TM_X = 128, TM_U = 256, TM_O = 384, TM_COLS = 512;   // S, X, U: two halves of PT, forward
-enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_P1 = 5, B_X = 6, B_P2 = 7, B_V = 8, B_P3 = 9, B_P4 = 10, B_OFREE = 11, B_DO = 12, B_OUT = 13, B_SST = 14, B_OST = 15, B_UST = 16, NBAR = 17 };
+enum { B_FULL = 0, B_EMPTY = 2, B_S = 4, B_P1 = 5, B_X = 6, B_P2 = 7, B_V = 8, B_P3 = 9, B_P4 = 10, B_OFREE = 11, B_DO = 12, B_OUT = 13, B_SST = 14, B_OST = 15, B_UST = 16, B_END = 17, NBAR = 18 };
 
 // Shared memory: a ring of two slots (the stacked k and q, [T; Pm], T's low
 // part, v or do, the decays), then the operand tiles the epilogues write.
@@ -173,6 +175,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(B_SST), 1);
         mbar_init(bar(B_OST), 1);
         mbar_init(bar(B_UST), 1);
+        mbar_init(bar(B_END), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -191,10 +194,12 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     };
 
     if (warp == W_PROD) {
-        // (stall: test only, nothing staged, every other role's wait runs out)
-        if (lane == 0 && !p.stall) {
+        if (lane == 0) {
             const int grp = (int)(h / (p.nheads / p.ngroups));
-            for (int c = 0; c < n; ++c) {
+            // (stall: test only, only its first chunks staged, every other role's wait runs out)
+            const int staged = p.stall && p.stall - 1 < n ? p.stall - 1 : n;
+            int c = 0;
+            for (; c < staged; ++c) {
                 if (!wait(B_EMPTY + (c & 1), (c >> 1) + 1)) break;
                 const uint32_t slot = base + (c & 1) * L::SLOT, fb = bar(B_FULL + (c & 1));
                 const int64_t ch = chunk_of(c), rec = bh * p.nchunks + ch;
@@ -211,6 +216,7 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tma_load_4d(slot + L::V, &tm_v, fb, pt * PT, (int)h, t0, (int)b);
                 bulk_load(slot + L::F, rg + REC_F, 3 * C * 4, fb);
             }
+            for (int d = c < 2 ? 0 : c - 2; d < c; ++d) drain(bar(B_FULL + (d & 1)), d >> 1, &g_gdr_dev_err);
         }
     } else if (warp == W_MMA) {
         {
@@ -274,8 +280,8 @@ gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
                 commit_elect(bar(B_EMPTY + (c & 1)));
             }
-            // the last commit must land before the CTA may exit
-            if (live) mwait(B_EMPTY + ((n - 1) & 1), (n - 1) >> 1);
+            commit_elect(bar(B_END));                      // behind every product and commit before it
+            drain(bar(B_END), 0, &g_gdr_dev_err);
         }
     } else if (warp == W_STORE) {
         // Per chunk: the state's tile, then o of the chunk before and u (backward:

@@ -153,6 +153,12 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, u
     }
 }
 
+// Before a role that issued copies or products leaves: wait (again with the
+// limit) for the last phase of `bar`, which they complete, whether or not some
+// wait gave up.  Shared memory is handed on when the CTA exits, TMEM when it is
+// freed, and neither may have anything on its way to it then.
+__device__ __forceinline__ void drain(uint32_t bar, int phase, unsigned int* err) { mbar_wait_sleep(bar, (uint32_t)phase & 1u, err); }
+
 // Whole warp: 16 consecutive 32-bit columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

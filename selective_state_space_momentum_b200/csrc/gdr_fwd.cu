@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128, 4) gdr_prep_kernel(const __grid_constant_
         mbar_init(bar, 1);
         fence_barrier_init();
         const int grp = h0 / (int)(p.nheads / p.ngroups);
-        if (!p.stall) {                                      // (test only: nothing staged, the wait runs out)
+        if (p.stall != 1) {                                  // (test only: nothing staged, the wait runs out)
             mbar_expect_tx(bar, 2 * C * RB);
 #pragma unroll
             for (int s = 0; s < DK / 64; ++s) {

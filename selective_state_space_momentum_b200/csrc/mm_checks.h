@@ -57,4 +57,12 @@ inline int inject_stall() {
     return (v && std::strcmp(v, "stall") == 0) ? 1 : 0;
 }
 
+// The same for the gated delta rule's kernels after a start:
+// MMSCAN_FAULT_INJECT=stall-late stages the first two chunks (heads) of a CTA,
+// so that the waits run out with copies and products issued.  GDRArgs::stall.
+inline int inject_gdr_stall() {
+    const char* v = std::getenv("MMSCAN_FAULT_INJECT");
+    return (v && std::strcmp(v, "stall-late") == 0) ? 3 : inject_stall();
+}
+
 }  // namespace mmscan

@@ -246,7 +246,7 @@ struct GDRArgs {
     float* dh0;            // (batch, H, P, N) or null
     void* dstates;         // laid out like states: the gradient reaching the state at a chunk's end
     void* dr;              // laid out like u: T^T du
-    int stall;             // test only: stage no input, so that the bounded waits run out
+    int stall;             // test only, if not 0: stage the first stall - 1 chunks (heads) of a CTA and no more, so that the bounded waits run out
 };
 
 // Arguments of one decode step of the gated delta rule.

@@ -117,7 +117,7 @@ mm_status check_workspace(const void* ws, size_t have, int64_t need) {
 mmscan::GDRArgs gdr_args(const mm_gdr_dims* d, const GdrSizes& z, float scale) {
     mmscan::GDRArgs a{};
     a.batch = d->batch; a.seqlen = d->seqlen; a.nheads = d->nheads; a.ngroups = d->ngroups;
-    a.stall = mmscan::inject_stall();
+    a.stall = mmscan::inject_gdr_stall();
     a.nchunks = z.nchunks; a.headdim = (int)d->headdim; a.dstate = (int)d->dstate; a.scale = scale;
     return a;
 }
