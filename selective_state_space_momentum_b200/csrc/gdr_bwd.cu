@@ -57,7 +57,9 @@ namespace {
 // Roles (19 warps): 0-15 the epilogues, then one for the loads and the stores,
 // one for the products, and one that sums up a head's decays before and its dg
 // and dbeta after.  Loads are issued in the order of need, k and q (into the
-// tile that the last item's dq and dk leave from) before S and dS'.
+// tile that the last item's dq and dk leave from) before S and dS'.  Waits are
+// bounded as in the chain, and the two warps that issue copies and products see
+// them complete before they leave.
 //
 // Bound: the latency of one chunk's steps (one CTA an SM: 190 KB of tiles and
 // all of TMEM at P = N = 128): the last item's store, k and q, two products,
@@ -68,7 +70,7 @@ namespace {
 constexpr int SLAB = 128 * 128;                        // 64 columns of a stacked tile
 constexpr int GEPI = 16, NP = GEPI / 4, G_LOAD = GEPI, G_MMA = GEPI + 1, G_AUX = GEPI + 2, GTHREADS = 32 * (GEPI + 3);
 // (B_CUM, B_ROWS: by head parity; B_RO, B_ST, B_FREE: by slot)
-enum { B_QK = 0, B_G = 1, B_YZ = 2, B_YZF = 3, B_AP = 4, B_ACC = 5, B_DONE = 6, B_CUM = 7, B_ROWS = 9, B_RO = 11, B_ST = 13, B_FREE = 15, NGBAR = 17 };
+enum { B_QK = 0, B_G = 1, B_YZ = 2, B_YZF = 3, B_AP = 4, B_ACC = 5, B_DONE = 6, B_CUM = 7, B_ROWS = 9, B_RO = 11, B_ST = 13, B_FREE = 15, B_END = 17, NGBAR = 18 };
 
 template <int DK, int DV>
 struct GradSmem {
@@ -118,7 +120,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int* wide = reinterpret_cast<int*>(sm + L::WIDE);
     auto bar = [&](int i) { return base + L::BAR + 8u * (uint32_t)i; };
     if (tid == 0) {
-        const int counts[NGBAR] = {1, 1, 1, GEPI, GEPI, 1, GEPI, 1, 1, GEPI, GEPI, 1, 1, 1, 1, GEPI + 1, GEPI + 1};
+        const int counts[NGBAR] = {1, 1, 1, GEPI, GEPI, 1, GEPI, 1, 1, GEPI, GEPI, 1, 1, 1, 1, GEPI + 1, GEPI + 1, 1};
         for (int i = 0; i < NGBAR; ++i) mbar_init(bar(i), counts[i]);
         *abort_flag = 0;
         fence_barrier_init();
@@ -145,7 +147,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     };
 
     if (w == G_LOAD) {
-        if (lane == 0 && !p.stall) {                         // (stall: test only, nothing staged, every wait runs out)
+        if (lane == 0) {                                     // (stall: test only, only the first heads staged, every wait runs out)
             // dq, dk of item m, staged in the tile of k and q (rows past L are clipped)
             auto store = [&](int m) -> bool {
                 if (!wait(B_DONE, m)) return false;
@@ -160,11 +162,15 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 return true;
             };
             bool live = true;
-            int n = 0;
+            int n = 0, qks = 0, ros = 0, sts = 0;              // loads issued: items' k and q, heads' tiles, heads' S and dS'
             for (int m = 0; m < items && live; ++m) {
                 const Item x = item_of(m);
                 for (int hh = 0; hh < hpg; ++hh, ++n) {
                     const int sl = n % L::NS, h = x.grp * hpg + hh;
+                    if (p.stall && n == p.stall - 1) {
+                        live = false;
+                        break;
+                    }
                     if (n >= L::NS && !(live = wait(B_FREE + sl, n / L::NS - 1))) break;
                     const int64_t rec = (x.b * p.nheads + h) * p.nchunks + x.ch;
                     const uint32_t slot = base + L::SLOTS0 + sl * L::SLOT, ro = bar(B_RO + sl), st = bar(B_ST + sl);
@@ -177,6 +183,7 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     }
                     bulk_load(slot + L::U, static_cast<const unsigned char*>(p.u) + rec * TV * (SLAB / 2), TV * (SLAB / 2), ro);
                     bulk_load(slot + L::F, static_cast<const unsigned char*>(p.rec) + rec * REC_BYTES + REC_F, 3 * C * 4, ro);
+                    ++ros;
                     if (hh == 0) {                           // k and q, once the tile has given up the last item's dq and dk: before
                                                              // S and dS', which are needed last (a store queues behind the loads)
                         if (m > 0 && !(live = store(m - 1))) break;
@@ -186,13 +193,18 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                             tma_load_4d(base + L::KQ + s * SLAB, &tm_k, bar(B_QK), 64 * s, x.grp, x.t0, (int)x.b);
                             tma_load_4d(base + L::KQ + s * SLAB + SLAB / 2, &tm_q, bar(B_QK), 64 * s, x.grp, x.t0, (int)x.b);
                         }
+                        ++qks;
                     }
                     mbar_expect_tx(st, 2 * DV * DK * 2);
                     bulk_load(slot + L::S, static_cast<const unsigned char*>(p.states) + rec * DV * DK * 2, DV * DK * 2, st);
                     bulk_load(slot + L::DS, static_cast<const unsigned char*>(p.dstates) + rec * DV * DK * 2, DV * DK * 2, st);
+                    ++sts;
                 }
             }
             if (live) store(items - 1);                      // (read out of shared memory: it is the kernel's end that completes it)
+            for (int x = ros < L::NS ? 0 : ros - L::NS; x < ros; ++x) drain(bar(B_RO + x % L::NS), x / L::NS, &g_grad_dev_err);
+            for (int x = sts < L::NS ? 0 : sts - L::NS; x < sts; ++x) drain(bar(B_ST + x % L::NS), x / L::NS, &g_grad_dev_err);
+            if (qks > 0) drain(bar(B_QK), qks - 1, &g_grad_dev_err);
         }
     } else if (w == G_MMA) {
         const uint32_t kq = base + L::KQ, ap = base + L::AP;
@@ -235,7 +247,8 @@ gdr_bwd_grad_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 commit_elect(bar(B_ACC));
             }
         }
-        if (live) wwait(B_ACC, (heads - 1) & 1);             // the last commit must land before the CTA may exit
+        commit_elect(bar(B_END));                            // behind every product and commit before it
+        drain(bar(B_END), 0, &g_grad_dev_err);
     } else if (w == G_AUX) {
         auto decays = [&](int n) {
             const Item x = item_of(n / hpg);

@@ -27,7 +27,7 @@ def _branch(src, head):
 
 
 def _ends_with_drain(block):
-    """The last statement of the innermost lane-0 block, outside every loop and condition but `for`, is a drain."""
+    """The block's last statement is a drain that no earlier wait's outcome guards."""
     block = re.sub(r"//[^\n]*", "", block).rstrip()
     while block.endswith("}"):                      # the blocks that end here: `if (lane == 0) { ... }` or a plain scope
         block = block[:-1].rstrip()
@@ -35,7 +35,8 @@ def _ends_with_drain(block):
     return "drain(" in last and "live" not in last and "abort" not in last
 
 
-ROLES = [("gdr_chain.cu", "if (warp == W_PROD) {"), ("gdr_chain.cu", "else if (warp == W_MMA) {")]
+ROLES = [("gdr_chain.cu", "if (warp == W_PROD) {"), ("gdr_chain.cu", "else if (warp == W_MMA) {"),
+         ("gdr_bwd.cu", "if (w == G_LOAD) {"), ("gdr_bwd.cu", "else if (w == G_MMA) {")]
 
 
 @pytest.mark.parametrize("name, head", ROLES, ids=lambda x: x.split("==")[-1].strip(" ){") if "==" in x else x)
