@@ -114,7 +114,10 @@ __global__ void __launch_bounds__(128, 4) gdr_prep_kernel(const __grid_constant_
         *reinterpret_cast<float2*>(fout + 2 * C + r) = be;
     }
     __syncthreads();
-    if (!__syncthreads_and(mbar_wait_sleep(bar, 0, &g_prep_dev_err))) return;
+    if (!__syncthreads_and(mbar_wait_sleep(bar, 0, &g_prep_dev_err))) {
+        if (tid == 0 && p.stall != 1) drain(bar, 0, &g_prep_dev_err);   // (the copies, if they were issued)
+        return;
+    }
 
     // k.k and q.k, n-tiles up to the diagonal
     float kk[8][4], qk[8][4];

@@ -45,3 +45,10 @@ def test_roles_wait_for_what_they_issued(name, head):
         src = f.read()
     block = _branch(src, head)
     assert _ends_with_drain(block), f"{name}: {head} leaves without waiting"
+
+
+def test_preparing_kernel_waits_for_its_copies():
+    with open(os.path.join(CSRC, "gdr_fwd.cu")) as f:
+        src = f.read()
+    block = _branch(src, "if (!__syncthreads_and(mbar_wait_sleep(bar, 0, &g_prep_dev_err))) {")
+    assert "drain(bar, 0" in block and block.index("drain(") < block.index("return")
