@@ -1,0 +1,99 @@
+"""GPU parity of the gated delta rule against the 64-bit recurrence, relative to
+whole tensors' norms: the bounds of tests/gdr_rounded.py, which do not grow over
+chunks (tests/test_gdr_rounded.py shows on the CPU what they refuse).  Up to 32
+chunks, with and without decay; calls large enough for every way the kernels
+share work: CTAs of the preparing kernel that take two and four heads, CTAs of
+the gradients' kernel that go on to further items.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import selective_state_space_momentum_b200 as mm  # noqa: E402
+from tests import gdr_plain as plain  # noqa: E402
+from tests import gdr_rounded as rounded  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["random", "no_decay", "strong_decay", "resets", "same_keys", "beta_edges", "zero_keys"]
+# batch, L, H, G, P, N: 1, 3, 8 and 32 chunks, every width
+SHAPES = [(2, 60, 4, 2, 64, 64), (1, 190, 4, 1, 128, 64), (2, 512, 2, 2, 64, 128), (1, 2040, 2, 1, 128, 128)]
+
+
+def _reference(q, k, v, g, beta, do, h0, dhT):
+    o, hT = plain.forward(q, k, v, g, beta, h0)
+    want = {"o": o, "hT": hT, **plain.backward(q, k, v, g, beta, do, h0=h0, dhT=dhT)}
+    o, hT, kept = rounded.forward(q, k, v, g, beta, h0)
+    return want, {"o": o, "hT": hT, **rounded.backward(kept, do, q.shape[2], dhT)}
+
+
+def _run(q, k, v, g, beta, do, h0, dhT):
+    o, hT, ckpt = mm.gdr_fwd_train(q, k, v, g, beta, h0=h0, return_last_state=True)
+    got = {"o": o, "hT": hT, **mm.gdr_bwd(q, k, v, g, beta, ckpt, do, dhT=dhT, return_dh0=True)}
+    mm.mm_device_status()
+    return got
+
+
+def _call(shape, kind, seed):
+    *qkvgb, h0 = plain.inputs(*shape, seed=seed, device="cuda", kind=kind, carry=True)
+    gen = torch.Generator().manual_seed(seed)
+    do = torch.randn(qkvgb[2].shape, generator=gen).cuda().to(torch.bfloat16)
+    dhT = torch.randn(h0.shape, generator=gen).cuda()
+    return [*qkvgb, do, h0, dhT]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_against_the_definition(shape, kind):
+    args = _call(shape, kind, seed=31 + shape[1])
+    got = _run(*args)
+    o, hT = mm.gdr_fwd(*args[:5], h0=args[6])
+    assert torch.equal(o, got["o"]) and torch.equal(hT, got["hT"])
+    rounded.check(got, *_reference(*args), shape[1], f"{shape} {kind}")
+
+
+def _heads(x, b, h, n):
+    return x[b:b + 1, :, h:h + n].contiguous()
+
+
+# heads of a group: 2 and 4 (as many to a CTA of the preparing kernel), 3 (one each)
+@pytest.mark.parametrize("per_group, H", [(2, 32), (4, 64), (3, 12)])
+@pytest.mark.parametrize("P", [64, 128])
+@pytest.mark.parametrize("N", [64, 128])
+def test_large_calls(P, N, per_group, H):
+    """38 chunks, the last of 5 steps: 1216 (304 at three heads) items of batch row, group and
+    chunk, eight (two) rounds of 148 and a part of one.  Sampled groups against the definition, and
+    the same bits as in a call of their own, which is small."""
+    L, G = 2373, H // per_group
+    chunks, items = 2 * H * 38, 2 * G * 38
+    assert items > 2 * 148 and items % 148 and (per_group == 3 or 2 * 4 * 148 * per_group <= chunks)
+    q, k, v, g, beta, do, h0, dhT = _call((2, L, H, G, P, N), "random", seed=P + N + H)
+    got = _run(q, k, v, g, beta, do, h0, dhT)
+    for b, grp in ((0, 0), (1, G - 1), (0, G // 2)):
+        h, n = grp * per_group, per_group
+        part = [_heads(q, b, grp, 1), _heads(k, b, grp, 1), *(_heads(t, b, h, n) for t in (v, g, beta, do)),
+                h0[b:b + 1, h:h + n].contiguous(), dhT[b:b + 1, h:h + n].contiguous()]
+        mine = {x: _heads(t, b, *((grp, 1) if x in ("dq", "dk") else (h, n))) for x, t in got.items() if x not in ("hT", "dh0")}
+        mine.update({x: got[x][b:b + 1, h:h + n] for x in ("hT", "dh0")})
+        alone = _run(*part)
+        assert all(torch.equal(mine[x], alone[x]) for x in mine), [x for x in mine if not torch.equal(mine[x], alone[x])]
+        rounded.check(mine, *_reference(*part), L, f"{P} {N} {per_group} batch row {b} group {grp}")
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["forward", "backward"])
+def test_wait_runs_out_after_a_start(monkeypatch, backward):
+    """Only the first two chunks (heads) of a CTA staged: the bounded waits give up behind copies and
+    products that were issued and are complete, the status says so once, and the next call is right."""
+    args = _call((2, 330, 4, 1, 64, 128), "random", seed=9)
+    _, _, ckpt = mm.gdr_fwd_train(*args[:5], h0=args[6])
+    call = lambda: list(mm.gdr_bwd(*args[:5], ckpt, args[5], return_dh0=True).values()) if backward else list(mm.gdr_fwd(*args[:5], h0=args[6]))
+    want = [t.clone() for t in call()]
+    monkeypatch.setenv("MMSCAN_FAULT_INJECT", "stall-late")
+    call()
+    monkeypatch.delenv("MMSCAN_FAULT_INJECT")
+    with pytest.raises(mm.MMError) as ei:
+        mm.mm_device_status()
+    assert ei.value.name == "MM_ERR_DEVICE_TIMEOUT", str(ei.value)
+    mm.mm_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    mm.mm_device_status()
