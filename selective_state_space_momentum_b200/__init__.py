@@ -696,9 +696,9 @@ def _side(stream, like):
     """The torch stream behind a wrapper's ``stream`` argument (an integer: a
     stream of the device that holds `like`, 0 its default one); None where that
     is the device's current stream."""
-    import torch
     if stream is None:
         return None
+    import torch
     device = like.device
     _on_cuda(device)
     if isinstance(stream, int):                              # (torch takes a handle of 0 for "none given")
@@ -713,20 +713,23 @@ def _pool(side):
     stream they run on.  A block that the current stream's pool hands out may
     have been freed there a moment ago, with work that uses it still queued,
     and nothing orders another stream behind that work."""
+    if side is None:
+        return _HERE
     import torch
-    return _HERE if side is None else torch.cuda.stream(side)
+    return torch.cuda.stream(side)
 
 
 def _give(side, *tensors):
     """Tensors from another stream's pool that a wrapper returns: the caller
     goes on with them on the current stream, so their memory may be handed out
     again only after that stream's work too."""
+    if side is None:
+        return
     import torch
-    if side is not None:
-        current = torch.cuda.current_stream(side.device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(current)
+    current = torch.cuda.current_stream(side.device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(current)
 
 
 def scan_fwd(x, delta, A, B, C, h0=None, v0=None, beta=0.9, alpha=1.0,
