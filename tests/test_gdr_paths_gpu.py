@@ -20,16 +20,16 @@ KINDS = ["random", "no_decay", "strong_decay", "resets", "same_keys", "beta_edge
 SHAPES = [(2, 60, 4, 2, 64, 64), (1, 190, 4, 1, 128, 64), (2, 512, 2, 2, 64, 128), (1, 2040, 2, 1, 128, 128)]
 
 
-def _reference(q, k, v, g, beta, do, h0, dhT):
-    o, hT = plain.forward(q, k, v, g, beta, h0)
-    want = {"o": o, "hT": hT, **plain.backward(q, k, v, g, beta, do, h0=h0, dhT=dhT)}
-    o, hT, kept = rounded.forward(q, k, v, g, beta, h0)
+def _reference(q, k, v, g, beta, do, h0, dhT, scale=None):
+    o, hT = plain.forward(q, k, v, g, beta, h0, scale)
+    want = {"o": o, "hT": hT, **plain.backward(q, k, v, g, beta, do, h0=h0, dhT=dhT, scale=scale)}
+    o, hT, kept = rounded.forward(q, k, v, g, beta, h0, scale)
     return want, {"o": o, "hT": hT, **rounded.backward(kept, do, q.shape[2], dhT)}
 
 
-def _run(q, k, v, g, beta, do, h0, dhT):
-    o, hT, ckpt = mm.gdr_fwd_train(q, k, v, g, beta, h0=h0, return_last_state=True)
-    got = {"o": o, "hT": hT, **mm.gdr_bwd(q, k, v, g, beta, ckpt, do, dhT=dhT, return_dh0=True)}
+def _run(q, k, v, g, beta, do, h0, dhT, scale=None):
+    o, hT, ckpt = mm.gdr_fwd_train(q, k, v, g, beta, h0=h0, scale=scale, return_last_state=True)
+    got = {"o": o, "hT": hT, **mm.gdr_bwd(q, k, v, g, beta, ckpt, do, dhT=dhT, scale=scale, return_dh0=True)}
     mm.mm_device_status()
     return got
 
@@ -50,6 +50,37 @@ def test_against_the_definition(shape, kind):
     o, hT = mm.gdr_fwd(*args[:5], h0=args[6])
     assert torch.equal(o, got["o"]) and torch.equal(hT, got["hT"])
     rounded.check(got, *_reference(*args), shape[1], f"{shape} {kind}")
+
+
+@pytest.mark.parametrize("scale", [0.75, -2.0, 0.0])
+def test_scale(scale):
+    args = _call((1, 150, 4, 2, 64, 128), "random", seed=77)
+    got = _run(*args, scale=scale)
+    rounded.check(got, *_reference(*args, scale=scale), 150, f"scale {scale}")
+
+
+@pytest.mark.parametrize("near", [0.9, 0.99, 1.0])
+def test_correlated_keys(near):
+    """Keys of one direction but for a part: k_i.k_j = near on average, beta = 1, little decay.  The
+    rows written are then small differences, and the roundings to bf16 weigh more."""
+    q, k, v, g, beta, do, h0, dhT = _call((2, 500, 4, 4, 64, 128), "random", seed=13)
+    k = near ** 0.5 * k[:, :1].double() + (1 - near) ** 0.5 * k.double()
+    k = (k / k.norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+    args = [q, k, v, (0.01 * g.double()).to(torch.bfloat16), torch.ones_like(beta), do, h0, dhT]
+    rounded.check(_run(*args), *_reference(*args), 500, f"keys {near}")
+
+
+def test_step_offsets_past_32_bits():
+    """A state of more than 2^31 elements: the last requests as in a call of their own."""
+    B, H, P, N = 4200, 64, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, v, g, beta = r(B, 2, N), r(B, 2, N), r(B, H, P), -r(B, H).abs(), r(B, H).sigmoid()
+    h = torch.randn(B, H, P, N, generator=gen, device="cuda")
+    assert h.numel() > 2 ** 31
+    few = [t[-3:].clone() for t in (q, k, v, g, beta, h)]
+    o = mm.gdr_step(q, k, v, g, beta, h)
+    assert torch.equal(mm.gdr_step(*few), o[-3:]) and torch.equal(few[5], h[-3:])
 
 
 def _heads(x, b, h, n):
