@@ -750,13 +750,18 @@ typedef struct {
  *          anything else until the call's work on `stream` has completed
  * The recurrence is stable for |k| <= 1 with beta in [0, 2]; k is not
  * normalised here.  The state is fp32: where it enters a matrix product it is
- * split in two bf16 terms, so hT is accurate to a few 1e-6 of its size; o
- * carries bf16 rounding of the products that reach it alone.  Padding a
+ * split in two bf16 terms, so hT is accurate to a few 1e-6 of its size.  o
+ * carries bf16 rounding of both operands of the products that reach it alone:
+ * 3e-3 of its norm, where its own rounding is 1.7e-3.  Where the keys of a chunk
+ * are nearly equal, beta near 1 and the decay weak, what a step writes is a
+ * small difference of larger sums and these roundings weigh more: with equal
+ * keys 4e-5 of hT and 1e-2 of o.  Padding a
  * batch row on the right changes nothing before the padding; its steps are
  * steps like any other for hT (give them beta = 0 and g = 0 to keep the state).
- * A NaN or infinity in q, k or v at a step reaches all outputs of its chunk of
- * 64 steps, those before it among them, and the chunks behind it; no chunk
- * before it, no other batch row and (from v) no other head.
+ * A NaN or infinity in q, k, v or beta, or a NaN in g, at a step reaches all
+ * outputs of its chunk of 64 steps, those before it among them, and the chunks
+ * behind it; no chunk before it, no other batch row and (from v, g and beta) no
+ * other head.
  * Streaming: calls split at a multiple of 64, with hT of the first as h0 of
  * the second, reproduce o and hT bit for bit.
  * Nothing is allocated; the calls can be captured into a CUDA graph (the
@@ -793,8 +798,9 @@ mm_status mm_gdr_bwd_workspace_size(const mm_gdr_dims *dims, size_t *bytes);
  * Outputs (overwritten): dq, dk (batch, L, G, N), summed over the heads of a
  * group; dv (batch, L, H, P); dg, dbeta (batch, L, H), all io; dh0 (batch, H,
  * P, N) fp32 or NULL.  Every output is bit-identical from run to run.
- * Products take their operands rounded to bf16, with fp32 sums; dh0, though
- * fp32, has that accuracy (a few 1e-3 of its size).
+ * Products take their operands rounded to bf16, with fp32 sums: the gradients
+ * are accurate to 3e-3 to 5e-3 of their norms, dh0, though fp32, to a few 1e-3.
+ * With nearly equal keys (see mm_gdr_fwd) dq to 1e-2, dv, dg and dbeta to 4e-2.
  * Errors: as mm_gdr_fwd.
  */
 mm_status mm_gdr_bwd(const void *q, const void *k, const void *v,

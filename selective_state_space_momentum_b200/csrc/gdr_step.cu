@@ -11,11 +11,13 @@
 // o = scale ((e^g S) q + u (k . q)), so that both are formed in one pass over
 // the loaded row and one shuffle reduction serves both).  All arithmetic is
 // fp32.  Eight lanes a row (16 above 128 states) and 12 blocks an SM keep 96 KB
-// of states in flight.  Measured: 175 us for 512 requests of 32 heads of 64 x 128
-// (6.2 TB/s), 3.2 us for one request of 32 heads of 128 x 128.  With 8 blocks an
-// SM (k kept in registers) 184, with loads and stores that stay in the caches
-// 194; after a flush of dirty lines, against 202 with 12 blocks: 216 with 16
-// (spills), 222 with 8, 242 with 16 lanes a row, 294 with 32, 236 with 4.
+// of states in flight.  Measured for 512 requests of 32 heads of 64 x 128: 176 us a
+// step in a row (6.1 TB/s; in a graph 175), 187 to 190 with cold caches, 205 right
+// behind 256 MB of other writes, which still leave L2 then; 3.2 us for one request
+// of 32 heads of 128 x 128.  With 8 blocks an SM (k kept in registers) 184 against
+// 175, with loads and stores that stay in the caches 194; behind the writes,
+// against 202 with 12 blocks: 216 with 16 (spills), 222 with 8, 242 with 16 lanes
+// a row, 294 with 32, 236 with 4.
 #include "mm_common.cuh"
 #include "mm_internal.h"
 

@@ -111,6 +111,24 @@ def test_large_calls(P, N, per_group, H):
         rounded.check(mine, *_reference(*part), L, f"{P} {N} {per_group} batch row {b} group {grp}")
 
 
+@pytest.mark.parametrize("where, value", [("g", float("nan")), ("beta", float("nan")), ("beta", float("inf"))])
+@pytest.mark.parametrize("H", [4, 64])
+def test_bad_decay_or_strength_stays_in_its_chunk_and_head(where, value, H):
+    """As for v: nothing before the chunk, no other batch row, no other head, also where a CTA of the
+    preparing kernel takes four heads (64 heads in 16 groups)."""
+    L, G = (200, 2) if H == 4 else (2373, 16)
+    q, k, v, g, beta, _, _, _ = _call((2, L, H, G, 64, 128), "random", seed=5)
+    clean, clean_h = mm.gdr_fwd(q, k, v, g, beta)
+    bad = {"g": g.clone(), "beta": beta.clone()}
+    bad[where][0, 100, 1] = value
+    o, hT = mm.gdr_fwd(q, k, v, bad["g"], bad["beta"])
+    mm.mm_device_status()
+    others = [h for h in range(H) if h != 1]
+    assert torch.equal(o[:, :64], clean[:, :64]) and torch.equal(o[1], clean[1]) and torch.equal(hT[1], clean_h[1])
+    assert torch.equal(o[0][:, others], clean[0][:, others]) and torch.equal(hT[0, others], clean_h[0, others])
+    assert not bool(torch.isfinite(o[0, 101:, 1].float()).any()) and not bool(torch.isfinite(hT[0, 1]).any())
+
+
 @pytest.mark.parametrize("backward", [False, True], ids=["forward", "backward"])
 def test_wait_runs_out_after_a_start(monkeypatch, backward):
     """Only the first two chunks (heads) of a CTA staged: the bounded waits give up behind copies and
