@@ -701,10 +701,12 @@ def _side(stream, like):
     import torch
     device = like.device
     _on_cuda(device)
-    if isinstance(stream, int):                              # (torch takes a handle of 0 for "none given")
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    elif stream.device != device:
+    if getattr(stream, "device", device) != device:
         raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+    if not isinstance(stream, torch.cuda.Stream):            # a handle, or an object that has one
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # (torch takes a handle of 0 for "none given")
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     return None if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream else stream
 
 

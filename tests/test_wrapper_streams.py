@@ -214,3 +214,10 @@ def test_split_over_ranks_orders_the_collective(stage, monkeypatch):
     mm.scan_fwd_split(*_scan(), 32, 128, stream=_Stream(77))
     assert order == [(11, 77), "gather", (77, 11)]
     assert (gathered[0].data_ptr(), 77) in stage.recorded and set(stage.made.values()) == {77}
+
+
+def test_an_object_that_only_has_a_handle(stage):
+    class Foreign:
+        cuda_stream = 77
+    _check(stage, NEW["gdr_step"], Foreign(), 77)
+    _check(stage, EARLIER["scan_fwd"], Foreign(), 77)
